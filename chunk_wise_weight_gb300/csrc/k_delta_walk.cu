@@ -186,8 +186,11 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t st, const
   for (int r = r0; r < n; r += 2, p += 2 * st) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(src + r * 256 + c * 16);
 }
 
+// out_ready: one a stage, since a stage's next phase waits for the storing warp to
+// have released it; with one for both, the chunk after could complete its phase
+// before that warp looks, and a wait by parity would miss both.
 struct TcBars {
-  uint64_t full[2], empty[2], out_ready, out_free;
+  uint64_t full[2], empty[2], out_ready[2], out_free;
   uint64_t s_ready, x_ready, w_ready, u_ready;         // operands in tensor memory
   uint64_t p_done, q_done, e_done, d_done, m_done;     // products
   uint32_t tmem;
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
     }
     uint64_t* ready[] = {&bars->s_ready, &bars->x_ready, &bars->w_ready, &bars->u_ready};
     for (uint64_t* r : ready) mbar_init(r, kTcWarps);
-    mbar_init(&bars->out_ready, kTcWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->out_ready[i], kTcWarps);
     mbar_init(&bars->out_free, 1);
     uint64_t* done[] = {&bars->p_done, &bars->q_done, &bars->e_done, &bars->d_done, &bars->m_done};
     for (uint64_t* d : done) mbar_init(d, 1);
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       unsigned char* u = a.save.u + (chunk0 * a.Hv + h) * token_tiles(a.dv) + row0 * 128;
       for (int c = 0; c < nchunks; ++c, u += a.Hv * token_tiles(a.dv)) {
         const int st = c & 1;
-        wait(&bars->out_ready, st);
+        wait(&bars->out_ready[st], (c >> 1) & 1);
         if (lane == 0) {
           bulk_store(u, smem + st * W::kTiles + W::kE, rows * 128);
           bulk_store(u + int64_t(a.dv) * 128, smem + 2 * W::kTiles + st * W::kRest + W::kV, rows * 128);
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       auto* out = static_cast<__nv_bfloat16*>(a.out) + ((b * a.T + tok0) * a.Hv + h) * a.dv + row0;
       const int64_t step = int64_t(a.Hv) * a.dv;
       for (int c = 0; c < nchunks; ++c, out += kDeltaChunk * step) {
-        wait(&bars->out_ready, c & 1);
+        wait(&bars->out_ready[c & 1], (c >> 1) & 1);
         store_rows(out, step, smem + W::kOut, pieces, min(kDeltaChunk, len - c * kDeltaChunk), lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->out_free);
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
 #pragma unroll
         for (int e = 0; e < kTok; ++e) *reinterpret_cast<__nv_bfloat16*>(to + e * 256) = __float2bfloat16_rn(O[e]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->out_ready);
+        if (lane == 0) mbar_arrive(&bars->out_ready[c & 1]);
       } else {
         const int n = min(kDeltaChunk, len - c * kDeltaChunk) - kTok * quarter;
         float* out = static_cast<float*>(a.out) +
@@ -554,7 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         stage_pieces(smem + 2 * W::kTiles + st * W::kRest + W::kV, row, 2 * quarter, ur[1]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->out_ready);
+        if (lane == 0) mbar_arrive(&bars->out_ready[st]);
       } else {
         if (lane == 0) mbar_arrive(&bars->empty[st]);  // V and the gates are read
       }
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       mbar_init(&bars->full[i], 3);
       mbar_init(&bars->empty[i], kTcWarps + 2);
     }
-    uint64_t* ready[] = {&bars->s_ready, &bars->x_ready, &bars->w_ready, &bars->u_ready, &bars->out_ready};
+    uint64_t* ready[] = {&bars->s_ready, &bars->x_ready, &bars->w_ready, &bars->u_ready, &bars->out_ready[0], &bars->out_ready[1]};
     for (uint64_t* r : ready) mbar_init(r, kTcWarps);
     uint64_t* done[] = {&bars->p_done, &bars->q_done, &bars->e_done, &bars->d_done};
     for (uint64_t* d : done) mbar_init(d, 1);
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       auto* out = a.dvp + ((b * a.T + tok0 + c0) * a.Hv + h) * a.dv + row0;
       for (int it = 0; it < nchunks; ++it, out -= kDeltaChunk * step) {
         const int c = nchunks - 1 - it, st = it & 1;
-        wait(&bars->out_ready, it & 1);
+        wait(&bars->out_ready[st], (it >> 1) & 1);
         if (lane < 2)
           bulk_store(a.dx + ((chunk0 + c) * a.Hv + h) * token_tiles(a.dv) + (int64_t(lane) * a.dv + row0) * 128,
                      smem + st * W::kTiles + W::kM + lane * 16384, rows * 128);
@@ -924,7 +927,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       for (int e = 0; e < kTok; ++e) *reinterpret_cast<__nv_bfloat16*>(col + e * 256) = __float2bfloat16_rn(x[e]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->out_ready);
+      if (lane == 0) mbar_arrive(&bars->out_ready[st]);
       // dR.E and dV.V over the rows
 #pragma unroll
       for (int e = 0; e < kTok; e += 2) {

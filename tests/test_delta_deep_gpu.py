@@ -1,0 +1,77 @@
+"""The gated delta rule and its gradients over many chunks: every two-stage ring
+is refilled several times, the barriers' phases return to where they began, and
+the states and their gradients are carried far.  Each case is on its intended
+side of the rule that picks whole heads or slices of 16 rows an SM.
+
+Tolerances: those of the shorter calls.  A chunk's rounding enters the state
+once and from then on decays with it (gates are negative, keys of length one),
+so the relative error of a long chain is that of a few chunks.
+"""
+import pytest
+import torch
+
+from chunk_wise_weight_gb300 import build, ittt
+import test_delta_gpu as seq
+import test_delta_grad_gpu as grad
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    torch.manual_seed(0)
+    build.build()
+    return ittt.load()
+
+
+def by_head(sequences, Hv, dv):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return dv > 32 and sequences * Hv * (dv // 16) > 2 * sms
+
+
+def heads_for(sequences, dv):
+    """The fewest value heads (a multiple of 2) with which the calls take whole heads."""
+    Hv = 2
+    while not by_head(sequences, Hv, dv):
+        Hv += 2
+    return Hv
+
+
+def both(x, S0, dS1, do, cu=None):
+    """Outputs (bf16 and fp32), states and gradients against the definition."""
+    dk = x["q"].shape[-1]
+    S1, dS0 = torch.empty_like(S0), torch.empty_like(S0)
+    out = seq.call(x, state_in=S0, state_out=S1, cu_seqlens=cu)
+    ref, rs = seq.reference(x, dk ** -0.5, S0, cu)
+    seq.check_out(out, ref)
+    seq.check_state(S1, rs)
+    seq.check_out(seq.call(x, state_in=S0, out_dtype=torch.float32, cu_seqlens=cu), ref)
+    got = grad.call(x, do, state_in=S0, grad_state_out=dS1, grad_state_in=dS0, cu_seqlens=cu)
+    grad.check((*got, dS0), grad.reference(x, dk ** -0.5, S0, do, dS1, cu))
+    again = grad.call(x, do, state_in=S0, grad_state_out=dS1, cu_seqlens=cu)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    return S1, dS0
+
+
+def inputs(B, S, T, Hk, Hv, dk, dv):
+    x = seq.make(B, T, Hk, Hv, dk, dv, seed=T)
+    return (x, 0.3 * torch.randn(S, Hv, dv, dk, device="cuda"), 0.1 * torch.randn(S, Hv, dv, dk, device="cuda"),
+            torch.randn(B, T, Hv, dv, device="cuda").bfloat16())
+
+
+@pytest.mark.parametrize("T,dk,dv", [(401, 64, 128), (401, 128, 64), (640, 128, 128)])
+def test_whole_heads(cuda_device, T, dk, dv):
+    Hv = heads_for(2, dv)
+    both(*inputs(2, 2, T, Hv // 2, Hv, dk, dv))
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 112), (64, 128)])
+def test_whole_heads_packed(cuda_device, dk, dv):
+    cu = [0, 0, 50, 230, 550, 934, 934, 1300]  # 0, 1, 3, 5, 6, 0 and 6 chunks
+    S = len(cu) - 1
+    Hv = heads_for(S, dv)
+    x, S0, dS1, do = inputs(1, S, cu[-1], Hv // 2, Hv, dk, dv)
+    S1, dS0 = both(x, S0, dS1, do, cu)
+    for s, (a, e) in enumerate(zip(cu, cu[1:])):
+        if a == e:
+            assert torch.equal(S1[s], S0[s]) and torch.equal(dS0[s], dS1[s])
