@@ -75,3 +75,19 @@ def test_whole_heads_packed(cuda_device, dk, dv):
     for s, (a, e) in enumerate(zip(cu, cu[1:])):
         if a == e:
             assert torch.equal(S1[s], S0[s]) and torch.equal(dS0[s], dS1[s])
+
+
+@pytest.mark.parametrize("T,Hk,Hv,dk,dv", [(450, 1, 2, 128, 48), (390, 2, 4, 64, 128)])
+def test_slices(cuda_device, T, Hk, Hv, dk, dv):
+    assert not by_head(2, Hv, dv)
+    both(*inputs(2, 2, T, Hk, Hv, dk, dv))
+
+
+def test_slices_in_pairs_packed(cuda_device):
+    """More slices than SMs, but not twice as many: two share a CTA."""
+    cu = [0, 400, 400, 430, 810]
+    sms, dv = torch.cuda.get_device_properties(0).multi_processor_count, 64
+    Hv = sms // (4 * 4) // 2 * 2 + 2
+    assert 4 * Hv * 4 > sms and not by_head(4, Hv, dv)
+    x, S0, dS1, do = inputs(1, 4, cu[-1], Hv // 2, Hv, 128, dv)
+    both(x, S0, dS1, do, cu)
