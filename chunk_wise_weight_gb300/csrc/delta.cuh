@@ -295,25 +295,22 @@ __device__ __forceinline__ void put_tiles(unsigned char* to, int ks, const float
 #pragma unroll
   for (int p = 0; p < NP; ++p) put_operand(to + (ks * NP + p) * kOperand, a[p], lane);
 }
-// A state's snapshot in parts, for the last kernel of the gradient: for each
-// panel of 128 rows of dv (the last may be shorter) and each part, pieces of 8
-// columns of dk, each [rows][16 bytes].  Neighbouring rows are neighbours in
-// memory (a warp whose lanes are rows stores without gaps), and eight rows of a
-// piece are a core matrix of an operand without swizzle.
-__host__ __device__ constexpr int64_t state_parts(int dv, int dk, int parts) { return int64_t(parts) * dv * dk * 2; }
+// A state as the gradient's last kernel reads it, three parts: for each panel of 64
+// rows of dv (the last may be shorter) and each part, pieces of 8 columns of dk, each
+// [rows][16 bytes].  Neighbouring rows are neighbours in memory (a warp whose lanes
+// are rows stores without gaps), and eight rows of a piece are a core matrix of an
+// operand without swizzle.
+constexpr int kPanel = 64;
+__host__ __device__ constexpr int64_t state_parts(int dv, int dk) { return int64_t(3) * dv * dk * 2; }
 template <int DK>
-__device__ __forceinline__ int64_t piece_at(int dv, int row, int parts, int part, int piece) {
-  const int panel = row >> 7, rows = min(128, dv - panel * 128);
-  return int64_t(panel) * parts * 128 * DK * 2 + (int64_t(part) * (DK / 8) + piece) * rows * 16 + (row & 127) * 16;
+__device__ __forceinline__ int64_t piece_at(int dv, int row, int part, int piece) {
+  const int panel = row / kPanel, rows = min(kPanel, dv - panel * kPanel);
+  return int64_t(panel) * 3 * kPanel * DK * 2 + (int64_t(part) * (DK / 8) + piece) * rows * 16 + (row % kPanel) * 16;
 }
-// A snapshot's bytes: two parts, then what is left of the 24 bits: a third part
-// (team walk), or the state itself in fp32 as [dk / 4][dv][4] (head walk).
-__host__ __device__ constexpr int64_t snap_bytes(int dv, int dk) { return state_parts(dv, dk, 4); }
 
-// This warp's columns of the state, as the left operand of the next chunk.
-// SNAP > 0: the first SNAP parts also go to the snapshot `snap`; `row` is the
-// slice's first row.
-template <int DK, int SNAP>
+// This warp's columns of the state, as the left operand of the next chunk.  SNAP:
+// its parts also go to `snap` (unless null); `row` is the slice's first row.
+template <int DK, bool SNAP>
 __device__ __forceinline__ void put_state(unsigned char* to, const float (&S)[DK / 32][4], int w, int lane,
                                           unsigned char* snap = nullptr, int row = 0, int dv = 0) {
 #pragma unroll
@@ -323,39 +320,15 @@ __device__ __forceinline__ void put_state(unsigned char* to, const float (&S)[DK
     split_frag<3>(S[2 * ks], S[2 * ks + 1], a);
 #pragma unroll
     for (int p = 0; p < 3; ++p) put_operand(to + (step * 3 + p) * kOperand, a[p], lane);
-    if (SNAP > 0 && snap != nullptr) {
+    if (SNAP && snap != nullptr) {
 #pragma unroll
-      for (int p = 0; p < SNAP; ++p)
+      for (int p = 0; p < 3; ++p)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // a[.][e]: rows + 8 (e & 1), pieces + (e >> 1)
-          unsigned char* at = snap + (p < 2 ? 0 : state_parts(dv, DK, 2)) +
-                              piece_at<DK>(dv, row + (lane >> 2), p < 2 ? 2 : 1, p < 2 ? p : 0, 2 * step + half) +
-                              4 * (lane & 3);
+          unsigned char* at = snap + piece_at<DK>(dv, row + (lane >> 2), p, 2 * step + half) + 4 * (lane & 3);
           *reinterpret_cast<uint32_t*>(at) = a[p][2 * half];
           *reinterpret_cast<uint32_t*>(at + 128) = a[p][2 * half + 1];
         }
-    }
-  }
-}
-// A warp's quarter of a slice of a state out of a snapshot of three parts.
-template <int DK>
-__device__ __forceinline__ void load_snapshot(float (&S)[DK / 32][4], const unsigned char* snap, int row,
-                                              int dv, int w, int lane) {
-#pragma unroll
-  for (int j = 0; j < DK / 32; ++j) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[j][e] = 0.f;
-#pragma unroll
-    for (int p = 2; p >= 0; --p) {
-      const unsigned char* at = snap + (p < 2 ? 0 : state_parts(dv, DK, 2)) +
-                                piece_at<DK>(dv, row + (lane >> 2), p < 2 ? 2 : 1, p < 2 ? p : 0, w * (DK / 32) + j) +
-                                4 * (lane & 3);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float2 v = unpack_bf16x2(__ldcs(reinterpret_cast<const unsigned int*>(at + 128 * half)));
-        S[j][2 * half] += v.x;
-        S[j][2 * half + 1] += v.y;
-      }
     }
   }
 }
@@ -552,18 +525,20 @@ __device__ __forceinline__ void store_tokens(const float (&T)[2][4], unsigned ch
         *reinterpret_cast<const uint4*>(box + r * 32 + half * 16);
 }
 
-// A warp's [16 dv x 16 tokens], two parts, into the tile of its rows: [2 parts]
-// [dv][64 tokens], 128-byte rows with swizzled pieces.
-__device__ __forceinline__ void store_token_parts(const uint32_t (&hi)[4], const uint32_t (&lo)[4],
-                                                  unsigned char* to, int dv, int row, int w, int lane) {
+// A warp's [16 dv x 16 tokens] into the tile of its rows: [3 parts][dv][64 tokens],
+// 128-byte rows with swizzled pieces.
+__device__ __forceinline__ void store_token_parts(const float (&T)[2][4], unsigned char* to, int dv, int row, int w,
+                                                  int lane) {
+  uint32_t a[3][4];
+  split_frag<3>(T[0], T[1], a);
   const int r = row + (lane >> 2);
   unsigned char* at = to + int64_t(r) * 128 + 4 * (lane & 3);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {  // rows + 8 (e & 1), pieces + (e >> 1)
-    unsigned char* d = at + (e & 1) * 1024 + (((2 * w + (e >> 1)) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint32_t*>(d) = hi[e];
-    *reinterpret_cast<uint32_t*>(d + int64_t(dv) * 128) = lo[e];
-  }
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // rows + 8 (e & 1), pieces + (e >> 1)
+      *reinterpret_cast<uint32_t*>(at + int64_t(p) * dv * 128 + (e & 1) * 1024 +
+                                   (((2 * w + (e >> 1)) ^ (r & 7)) << 4)) = a[p][e];
 }
 
 // A warp's 16 tokens of a [64 tokens][16 dv] column block, transposed: v[2i],
@@ -572,23 +547,21 @@ __device__ __forceinline__ void load_cols_t(uint32_t (&v)[4], uint32_t cols, int
   ldsm4_t(v, cols + (8 * (2 * w + (lane >> 4)) + (lane & 7)) * pitch + ((lane >> 3) & 1) * 16);
 }
 
-// x[2i + e] is the lane's share of the sum of token 8i + 2 (lane & 3) + e of
-// the warp's 16; sums over the lanes of equal lane & 3 and stores the results.
-__device__ __forceinline__ void store_token_sums(float (&x)[4], float* to, int lane) {
-  const bool up = lane & 16;
+// Sums of 16 numbers over the lanes of a warp; lanes 0, 2, .. 30 store them.
+__device__ __forceinline__ void store_row_sums(float (&x)[16], float* to, int lane) {
+  int m = 16;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float send = up ? x[i] : x[i + 2], keep = up ? x[i + 2] : x[i];
-    x[i] = keep + __shfl_xor_sync(~0u, send, 16);
+  for (int cnt = 8; cnt >= 1; cnt >>= 1, m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < cnt; ++i) {
+      const float send = up ? x[i] : x[i + cnt], keep = up ? x[i + cnt] : x[i];
+      x[i] = keep + __shfl_xor_sync(~0u, send, m);
+    }
   }
-#pragma unroll
-  for (int m = 8; m >= 4; m >>= 1)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] += __shfl_xor_sync(~0u, x[i], m);
-  if ((lane & 12) == 0)
-    *reinterpret_cast<float2*>(to + 8 * (lane >> 4) + 2 * (lane & 3)) = make_float2(x[0], x[1]);
+  x[0] += __shfl_xor_sync(~0u, x[0], 1);
+  if ((lane & 1) == 0) to[lane >> 1] = x[0];
 }
-
 // Slices a CTA of a walk: one while every slice has an SM of its own, two beyond
 // that, which share the loads of K, Q and the chunk's block and fill each other's
 // waits.  1024 tokens, heads of 128 x 128, one / two slices a CTA: 16 heads (128
@@ -612,34 +585,24 @@ cudaError_t launch_delta_prepare(const LaunchEnv& env, const DeltaArgs& a, unsig
 
 // What the gradient's forward walk keeps.
 struct DeltaSave {
-  HeadView dout;
-  // [nchunks + ndocs][Hv]: states at chunk starts, then the last one
-  unsigned char* snap;
-  // [nchunks][Hv]: E, transposed, as [dv][64] (team walk) or [64 / 4][dv][4]
-  float* e;
-  unsigned char* u;  // [nchunks][Hv][2 parts][dv][64]: U, transposed (see store_token_parts)
-  float* odot;       // [nchunks][Hv][row blocks][64]: dO.O over the rows of a block
+  unsigned char* snap;  // [nchunks][Hv]: the state at the chunk's start
+  unsigned char* e;     // [nchunks][Hv][3 parts][dv][64]: E, transposed (see store_token_parts)
 };
-__host__ __device__ constexpr int64_t token_tiles(int dv) { return int64_t(dv) * 2 * 128; }
+__host__ __device__ constexpr int64_t token_tiles(int dv) { return int64_t(dv) * 3 * 128; }
 
 // The gradient's reverse walk.
 struct ReverseArgs {
-  HeadView q, k, v, dout;
+  HeadView q, k, dout;
   int Hk, Hv, dv, T;
   DeltaMap map;
   float scale;
   const unsigned char* blocks;
   unsigned int* status;
-  const unsigned char* snap;
-  const float* e;
   const float* dstate_out;
   float* dstate_in;
   __nv_bfloat16* dvp;
-  unsigned char* dx;     // dX, laid out as U
-  unsigned char* dsnap;  // [nchunks][Hv]: dS' of each chunk, in two parts
-  float* vdot;           // [nchunks][Hv][row blocks][64]: dV.V
-  float* bdot;           // the same for dR.E
-  float* sdot;           // [nchunks][Hv][row blocks][4]: <dS', S'>
+  unsigned char* dr;     // dR, laid out as E
+  unsigned char* dsnap;  // [nchunks][Hv]: dS' of each chunk
 };
 
 // Whether the walks (forward; forward for the gradient; reverse) give an SM a whole

@@ -280,24 +280,24 @@ struct WalkArgs {
   bool out_fp32;
   const unsigned char* blocks;
   unsigned int* status;
-  DeltaSave save;  // SAVE only
+  DeltaSave save;  // NO = 0 only
 };
 
-// Shared memory of a CTA of `ns` slices: two stages (K, Q, E map, scores,
-// gates, V and, in the gradient's form, dO), then what each slice's warps
-// exchange.
-template <int DK, bool SAVE, int NO>
+// Shared memory of a CTA of `ns` slices: two stages (K, E map, gates, V, and for the
+// output Q and the scores), then what each slice's warps exchange.
+template <int DK, int NO>
 struct WalkShape {
   static constexpr int kTile = kDeltaChunk * DK * 2;
+  static constexpr int kMap = (NO ? 2 : 1) * kTile;
   static constexpr int kMaps = (3 + NO) * kImage;
-  static constexpr int kGate = 2 * kTile + kMaps;
+  static constexpr int kGate = kMap + kMaps;
   static constexpr int kCols = kGate + 1024;
   static constexpr int kX = DK / 16 * 3 * kOperand;  // operands of X, after the state's
   static constexpr int kW = kX + 12 * kOperand;      // of e^{G_63 - G} U
   static constexpr int kU = kW + 12 * kOperand;      // of U
   static constexpr int kOwn = kU + 4 * NO * kOperand;
   static __host__ __device__ constexpr int stage(int ns) {
-    return kCols + (SAVE ? 2 : 1) * kDeltaChunk * (2 * ns + 1) * 16;
+    return kCols + kDeltaChunk * (2 * ns + 1) * 16;
   }
   static __host__ __device__ constexpr int smem(int ns) {
     return 2 * stage(ns) + ns * kOwn + int(sizeof(StageBars));
@@ -305,15 +305,15 @@ struct WalkShape {
 };
 
 // One (sequence, head) and `ns` = blockDim.x / 128 slices of its dv rows, a team
-// of four warps each, and a warp that loads.  SAVE: the gradient's forward pass,
-// which keeps what the reverse walk reads (the states at the chunks' starts, E,
-// and dO.O) and writes no output.  NO: parts of the operands in the output's
-// products, two (16 bits) where it is rounded to bf16, three (24) where it is
-// fp32 and for dO.O, which takes part in differences.
-template <int DK, bool SAVE, int NO>
+// of four warps each, and a warp that loads.  NO: parts of the operands in the
+// output's products, two (16 bits) where it is rounded to bf16, three (24) where it is
+// fp32; 0: the gradient's forward pass, which writes no output and keeps the states at
+// the chunks' starts and E.
+template <int DK, int NO>
 __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  using W = WalkShape<DK, SAVE, NO>;
+  using W = WalkShape<DK, NO>;
+  constexpr bool SAVE = NO == 0;
   const int ns = blockDim.x / kTeam, tid = threadIdx.x, lane = tid & 31, slice = tid / kTeam;
   // the teams take their tokens in opposite orders: the triangle's long rows of
   // one share a scheduler with the short rows of the other
@@ -338,10 +338,6 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
     const auto* kp = static_cast<const __nv_bfloat16*>(a.k.data) + b * a.k.sb + tok0 * a.k.st + hk * a.k.sh;
     const auto* qp = static_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.sb + tok0 * a.q.st + hk * a.q.sh;
     const auto* vp = static_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + tok0 * a.v.st + h * a.v.sh + col0;
-    const __nv_bfloat16* dop = nullptr;
-    if constexpr (SAVE)
-      dop = static_cast<const __nv_bfloat16*>(a.save.dout.data) + b * a.save.dout.sb +
-            tok0 * a.save.dout.st + h * a.save.dout.sh + col0;
     for (int c = 0; c <= nchunks; ++c) {
       if (c < nchunks) {
         unsigned char* st = smem + (c & 1) * stage_bytes;
@@ -350,15 +346,12 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
         if (lane == 0) {
           const unsigned char* blk = a.blocks + ((chunk0 + c) * a.Hv + h) * int64_t(SAVE ? kBlkGrad : kBlkFwd);
           mbar_arrive_expect_tx(&bars->full[c & 1], W::kMaps + 768);
-          bulk_load(st + 2 * W::kTile, blk, W::kMaps, &bars->full[c & 1]);
+          bulk_load(st + W::kMap, blk, W::kMaps, &bars->full[c & 1]);
           bulk_load(st + W::kGate, blk + kBlkGate, 768, &bars->full[c & 1]);
         }
         warp_load_tile<DK / 8>(st, kp + t * a.k.st, a.k.st, n, a.k.vec, lane);
-        warp_load_tile<DK / 8>(st + W::kTile, qp + t * a.q.st, a.q.st, n, a.q.vec, lane);
+        if constexpr (!SAVE) warp_load_tile<DK / 8>(st + W::kTile, qp + t * a.q.st, a.q.st, n, a.q.vec, lane);
         load_cols(st + W::kCols, vp + t * a.v.st, a.v.st, pieces, n, a.v.vec, lane, 32);
-        if constexpr (SAVE)
-          load_cols(st + W::kCols + kDeltaChunk * pitch, dop + t * a.save.dout.st, a.save.dout.st, pieces,
-                    n, a.save.dout.vec, lane, 32);
         cp_wait_all();
       }
       __syncthreads();  // chunk c is in its stage; the teams are done with chunk c - 1
@@ -369,16 +362,15 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
   float S[DK / 32][4];
   const int64_t srow = (int64_t(s) * a.Hv + h) * a.dv + row0;
   load_state<DK>(S, a.state_in, srow, w, lane);
-  // a sequence of n chunks owns n + 1 snapshots
   auto snapshot = [&](int c) {
-    return SAVE ? a.save.snap + ((s + chunk0 + c) * a.Hv + h) * snap_bytes(a.dv, DK) : nullptr;
+    return SAVE && c < nchunks ? a.save.snap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK) : nullptr;
   };
-  put_state<DK, SAVE ? 3 : 0>(own, S, w, lane, snapshot(0), row0, a.dv);
+  put_state<DK, SAVE>(own, S, w, lane, snapshot(0), row0, a.dv);
   for (int c = 0; c < nchunks; ++c) {
     __syncthreads();
     wait_block(bars, c, a.status);
     const unsigned char* st = smem + (c & 1) * stage_bytes;
-    const uint32_t sk = smem_u32(st), se = sk + 2 * W::kTile;
+    const uint32_t sk = smem_u32(st), se = sk + W::kMap;
     const float* gate = reinterpret_cast<const float*>(st + W::kGate) + 16 * w + t2;  // this warp's tokens
     const int64_t ch = (chunk0 + c) * a.Hv + h;
     float X[2][4], O[2][4];
@@ -395,10 +387,12 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
         X[i][1] = v0.y - eg.y * X[i][1];
         X[i][2] = v1.x - eg.x * X[i][2];
         X[i][3] = v1.y - eg.y * X[i][3];
-        O[i][0] *= a.scale * eg.x;
-        O[i][1] *= a.scale * eg.y;
-        O[i][2] *= a.scale * eg.x;
-        O[i][3] *= a.scale * eg.y;
+        if constexpr (!SAVE) {
+          O[i][0] *= a.scale * eg.x;
+          O[i][1] *= a.scale * eg.y;
+          O[i][2] *= a.scale * eg.x;
+          O[i][3] *= a.scale * eg.y;
+        }
       }
       put_tiles<3>(own + W::kX, w, X[0], X[1], lane);
     }
@@ -409,14 +403,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
       team_bar(slice);
       map_tokens<false, 3>(own + W::kX, be, w, lane, U);  // E
     }
-    if constexpr (SAVE) {
-      float* e = a.save.e + (ch * a.dv + row0 + g4) * kDeltaChunk + 16 * w + t2;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        *reinterpret_cast<float2*>(e + 8 * i) = make_float2(U[i][0], U[i][1]);
-        *reinterpret_cast<float2*>(e + 8 * kDeltaChunk + 8 * i) = make_float2(U[i][2], U[i][3]);
-      }
-    }
+    if constexpr (SAVE) store_token_parts(U, a.save.e + ch * token_tiles(a.dv), a.dv, row0, w, lane);
     {
       // U = b E and e^{G_63 - G} U
       float V[2][4];
@@ -431,12 +418,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
         }
       }
       put_tiles<3>(own + W::kW, w, V[0], V[1], lane);
-      uint32_t ua[NO][4];
-      split_frag<NO>(U[0], U[1], ua);
-#pragma unroll
-      for (int p = 0; p < NO; ++p) put_operand(own + W::kU + (w * NO + p) * kOperand, ua[p], lane);
-      if constexpr (SAVE)
-        store_token_parts(ua[0], ua[1], a.save.u + ch * token_tiles(a.dv), a.dv, row0, w, lane);
+      if constexpr (!SAVE) put_tiles<NO>(own + W::kU, w, U[0], U[1], lane);
     }
     {
       uint32_t bk[4][DK / 64][4];
@@ -451,9 +433,9 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][e] = last * S[j][e] + acc[j][e];
       // every warp is past this chunk's
-      put_state<DK, SAVE ? 3 : 0>(own, S, w, lane, snapshot(c + 1), row0, a.dv);
+      put_state<DK, SAVE>(own, S, w, lane, snapshot(c + 1), row0, a.dv);
     }
-    {
+    if constexpr (!SAVE) {
       // O += M U, this warp's tokens
       uint32_t bm[4][NO][4];
       float T[2][4];
@@ -466,19 +448,8 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
     }
     const int n = min(kDeltaChunk, len - c * kDeltaChunk) - 16 * w;  // this warp's tokens, if any
     const int64_t orow = b * a.T + tok0 + int64_t(c) * kDeltaChunk + 16 * w;
-    if constexpr (SAVE) {
-      // dO.O over the slice's 16 rows, for each token
-      uint32_t v[4];
-      float x[4];
-      load_cols_t(v, sk + W::kCols + kDeltaChunk * pitch + 32 * slice, pitch, w, lane);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 v0 = unpack_bf16x2(v[2 * i]), v1 = unpack_bf16x2(v[2 * i + 1]);
-        x[2 * i] = v0.x * O[i][0] + v1.x * O[i][2];
-        x[2 * i + 1] = v0.y * O[i][1] + v1.y * O[i][3];
-      }
-      store_token_sums(x, a.save.odot + (ch * (a.dv / 16) + row0 / 16) * kDeltaChunk + 16 * w, lane);
-    } else if (a.out_fp32) {
+    if (SAVE) continue;
+    if (a.out_fp32) {
       float* out = static_cast<float*>(a.out);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -501,14 +472,14 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
   if (a.state_out) store_state<DK>(S, a.state_out, srow, w, lane);
 }
 
-template <int DK, bool SAVE, int NO>
+template <int DK, int NO>
 cudaError_t run_walk(const LaunchEnv& env, const WalkArgs& w) {
-  using W = WalkShape<DK, SAVE, NO>;
+  using W = WalkShape<DK, NO>;
   const int ns = walk_slices(w.map.ndocs, w.Hv, w.dv, env.num_sms);
-  const cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<DK, SAVE, NO>,
+  const cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<DK, NO>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, W::smem(2));
   if (e != cudaSuccess) return e;
-  return launch_pdl(delta_walk_kernel<DK, SAVE, NO>,
+  return launch_pdl(delta_walk_kernel<DK, NO>,
                     dim3(unsigned(w.map.ndocs * w.Hv * (w.dv / (16 * ns)))),
                     dim3(kTeam * ns + 32),
                     W::smem(ns), env.stream, w);
@@ -707,10 +678,10 @@ cudaError_t launch_team_walk(const LaunchEnv& env, const DeltaArgs& a, const uns
   w.status = env.status;
   if (save) {
     w.save = *save;
-    return a.dk == 64 ? run_walk<64, true, 3>(env, w) : run_walk<128, true, 3>(env, w);
+    return a.dk == 64 ? run_walk<64, 0>(env, w) : run_walk<128, 0>(env, w);
   }
-  if (a.out_fp32) return a.dk == 64 ? run_walk<64, false, 3>(env, w) : run_walk<128, false, 3>(env, w);
-  return a.dk == 64 ? run_walk<64, false, 2>(env, w) : run_walk<128, false, 2>(env, w);
+  if (a.out_fp32) return a.dk == 64 ? run_walk<64, 3>(env, w) : run_walk<128, 3>(env, w);
+  return a.dk == 64 ? run_walk<64, 2>(env, w) : run_walk<128, 2>(env, w);
 }
 
 cudaError_t launch_delta_chunked(const LaunchEnv& env, const DeltaArgs& a) {

@@ -7,17 +7,23 @@
 //   dR  = (I + diag(b) B)^-T dU0             gradient at b X
 //   dV  = b dR =: dX,   db_i = dR_i.E_i
 //   dS  = e^{G_63} dS' + scale (e^G dO)^T Q - (e^G dX)^T K
-//   dg_t = sum_{i >= t} (dO_i.O_i - dV_i.V_i) + <dS', S'>
 //   dq_i = scale e^{G_i} dO_i S + sum_{j <= i} scale D_ij (dO_i.U_j) k_j
 //   dk_j = sum_{i >= j} scale D_ij (dO_i.U_j) q_i - e^{G_j} dX_j S + e^{G_63 - G_j} U_j dS'
 //          - sum_{i < j} D_ji (dX_j.U_i) k_i - sum_{i > j} D_ij (dX_i.U_j) k_i
-// (dg: O, the scores and the corrections all scale with e^{G_i} as rows and
-// e^{-G_j} as columns, so the terms collapse to products with O and V.)
+//   dg_t = sum_{i >= t} a_i + sum_{i >= t > j} B_ij + sum_{j < t} c_j + e^{G_63} <dS', S>
+//          a_i = scale e^{G_i} dO_i S.q_i - e^{G_i} dX_i S.k_i
+//          B_ij = scale D_ij (dO_i.U_j) (q_i.k_j) - D_ij (dX_i.U_j) (k_i.k_j)
+//          c_j = e^{G_63 - G_j} U_j dS'.k_j
+// (dg_t gathers every decay that spans token t.  Each term carries its own decay and
+// none is subtracted from another, so dg is as exact in a head that forgets within a
+// token as in one that keeps thousands, and zero at a reset.  The sums telescope to
+// products of dO with O and dV with V, which cancel: at g = -12 a tenth of dg was lost.)
 //
-// Four kernels: the chunks' blocks and the forward walk (k_delta.cu) keep S, E
-// and dO.O; a reverse walk, of the same shape, carries dS and leaves dX and
-// dS'; then dq and dk of every chunk at once.  2 x 4096 tokens, 20 heads of
-// 128 x 128: 95 + 330 + 422 + 184 us; bound by the two walks' chains.
+// Four kernels: the chunks' blocks and the forward walk (k_delta.cu) keep S and E; a
+// reverse walk, of the same shape, carries dS and leaves dR and dS'; then everything
+// else, of every chunk at once.  2 x 4096 tokens, 20 heads of 128 x 128: 95 + 277 + 375 +
+// 379 us; bound by the two walks' chains and by the last kernel's passes, which follow one
+// another.
 #include <algorithm>
 
 #include "delta.cuh"
@@ -25,8 +31,8 @@
 namespace ittt {
 namespace {
 
-// Shared memory of a CTA of `ns` slices: two stages (K, Q, scores, gates, R map,
-// V, dO), then what each slice's warps exchange.
+// Shared memory of a CTA of `ns` slices: two stages (K, Q, scores, gates, R map, dO),
+// then what each slice's warps exchange.
 template <int DK>
 struct ReverseShape {
   static constexpr int kTile = kDeltaChunk * DK * 2;
@@ -39,7 +45,7 @@ struct ReverseShape {
   static constexpr int kY = kW + 12 * kOperand;      // of scale e^G dO
   static constexpr int kOwn = kY + 12 * kOperand;
   static __host__ __device__ constexpr int stage(int ns) {
-    return kCols + 2 * kDeltaChunk * (2 * ns + 1) * 16;
+    return kCols + kDeltaChunk * (2 * ns + 1) * 16;
   }
   static __host__ __device__ constexpr int smem(int ns) {
     return 2 * stage(ns) + ns * kOwn + int(sizeof(StageBars));
@@ -59,7 +65,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
   const int parts = a.dv / (16 * ns);
   const int h = (blockIdx.x / parts) % a.Hv, s = blockIdx.x / (parts * a.Hv);
   const int col0 = (blockIdx.x % parts) * 16 * ns, row0 = col0 + 16 * slice;
-  const int g4 = lane >> 2, t2 = 2 * (lane & 3);
+  const int t2 = 2 * (lane & 3);
   unsigned char* own = smem + 2 * stage_bytes + slice * W::kOwn;
   StageBars* bars = reinterpret_cast<StageBars*>(smem + 2 * stage_bytes + ns * W::kOwn);
   init_bars(bars);
@@ -73,7 +79,6 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
     const int hk = h / (a.Hv / a.Hk);
     const auto* kp = static_cast<const __nv_bfloat16*>(a.k.data) + b * a.k.sb + tok0 * a.k.st + hk * a.k.sh;
     const auto* qp = static_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.sb + tok0 * a.q.st + hk * a.q.sh;
-    const auto* vp = static_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + tok0 * a.v.st + h * a.v.sh + col0;
     const auto* dop = static_cast<const __nv_bfloat16*>(a.dout.data) + b * a.dout.sb + tok0 * a.dout.st + h * a.dout.sh + col0;
     for (int it = 0; it <= nchunks; ++it) {
       if (it < nchunks) {
@@ -88,8 +93,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
         }
         warp_load_tile<DK / 8>(st, kp + t * a.k.st, a.k.st, n, a.k.vec, lane);
         warp_load_tile<DK / 8>(st + W::kTile, qp + t * a.q.st, a.q.st, n, a.q.vec, lane);
-        load_cols(st + W::kCols, vp + t * a.v.st, a.v.st, pieces, n, a.v.vec, lane, 32);
-        load_cols(st + W::kCols + kDeltaChunk * pitch, dop + t * a.dout.st, a.dout.st, pieces, n, a.dout.vec, lane, 32);
+        load_cols(st + W::kCols, dop + t * a.dout.st, a.dout.st, pieces, n, a.dout.vec, lane, 32);
         cp_wait_all();
       }
       __syncthreads();
@@ -101,28 +105,18 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
   const int64_t srow = (int64_t(s) * a.Hv + h) * a.dv + row0;
   load_state<DK>(S, a.dstate_out, srow, w, lane);
   auto snapshot = [&](int c) {
-    return c < 0 ? nullptr : a.dsnap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK, 2);
+    return c < 0 ? nullptr : a.dsnap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK);
   };
-  put_state<DK, 2>(own, S, w, lane, snapshot(nchunks - 1), row0, a.dv);
+  put_state<DK, true>(own, S, w, lane, snapshot(nchunks - 1), row0, a.dv);
   for (int it = 0; it < nchunks; ++it) {
     const int c = nchunks - 1 - it;
     __syncthreads();
     wait_block(bars, it, a.status);
     const unsigned char* st = smem + (it & 1) * stage_bytes;
     const uint32_t sk = smem_u32(st), sq = sk + W::kTile;
-    const uint32_t sv = sk + W::kCols + 32 * slice, sd = sv + kDeltaChunk * pitch;
+    const uint32_t sd = sk + W::kCols + 32 * slice;
     const float* gate = reinterpret_cast<const float*>(st + W::kGate) + 16 * w + t2;  // this warp's tokens
     const int64_t ch = (chunk0 + c) * a.Hv + h;
-    // S', the state that the chunk ends with, and this warp's tokens of E: used later
-    float S1[DK / 32][4];
-    load_snapshot<DK>(S1, a.snap + ((s + chunk0 + c + 1) * a.Hv + h) * snap_bytes(a.dv, DK), row0, a.dv, w, lane);
-    float2 E[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        E[i][half] = *reinterpret_cast<const float2*>(
-            a.e + (ch * a.dv + row0 + g4 + 8 * half) * kDeltaChunk + 16 * w + 8 * i + t2);
     float X[2][4];
     {
       float none[2][4];
@@ -168,20 +162,19 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
       }
       put_tiles<3>(own + W::kX, w, X[0], X[1], lane);
     }
-    float R[2][4], x[4];
+    float R[2][4];
     {
       uint32_t br[4][3][4];
       load_map<true, 3>(br, sk + W::kR, w, lane);
       team_bar(slice);
       map_tokens<true, 3>(own + W::kX, br, w, lane, R);  // dR
     }
+    store_token_parts(R, a.dr + ch * token_tiles(a.dv), a.dv, row0, w, lane);
     {
-      // dR.E; dX = b dR; the operand of -e^G dX
+      // dX = dV = b dR; the operand of -e^G dX
       float y[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[2 * i] = R[i][0] * E[i][0].x + R[i][2] * E[i][1].x;
-        x[2 * i + 1] = R[i][1] * E[i][0].y + R[i][3] * E[i][1].y;
         const float2 be = *reinterpret_cast<const float2*>(gate + 128 + 8 * i);
         const float2 eg = *reinterpret_cast<const float2*>(gate + 8 * i);
 #pragma unroll
@@ -192,14 +185,6 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
       }
       put_tiles<3>(own + W::kW, w, y[0], y[1], lane);
     }
-    // <dS', S'>, this warp's columns
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < DK / 32; ++j)
-      dot += (S1[j][0] * S[j][0] + S1[j][1] * S[j][1]) + (S1[j][2] * S[j][2] + S1[j][3] * S[j][3]);
-#pragma unroll
-    for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
-    if (lane == 0) a.sdot[(ch * (a.dv / 16) + row0 / 16) * 4 + w] = dot;
     {
       uint32_t bk[4][DK / 64][4];
       load_rows<DK>(bk, sk, w, lane);
@@ -219,31 +204,13 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[j][e] += acc[j][e];
       // every warp is past this chunk's
-      put_state<DK, 2>(own, S, w, lane, snapshot(c - 1), row0, a.dv);
+      put_state<DK, true>(own, S, w, lane, snapshot(c - 1), row0, a.dv);
     }
-    // dV.V; dX for the last kernel, dV for the caller
-    {
-      uint32_t v[4];
-      float y[4];
-      load_cols_t(v, sv, pitch, w, lane);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 v0 = unpack_bf16x2(v[2 * i]), v1 = unpack_bf16x2(v[2 * i + 1]);
-        y[2 * i] = R[i][0] * v0.x + R[i][2] * v1.x;
-        y[2 * i + 1] = R[i][1] * v0.y + R[i][3] * v1.y;
-      }
-      uint32_t xa[2][4];
-      split_frag<2>(R[0], R[1], xa);
-      store_token_parts(xa[0], xa[1], a.dx + ch * token_tiles(a.dv), a.dv, row0, w, lane);
-      const int64_t at = (ch * (a.dv / 16) + row0 / 16) * kDeltaChunk + 16 * w;
-      store_token_sums(x, a.bdot + at, lane);
-      store_token_sums(y, a.vdot + at, lane);
-      const int n = min(kDeltaChunk, len - c * kDeltaChunk) - 16 * w;
-      const int64_t orow = b * a.T + tok0 + int64_t(c) * kDeltaChunk + 16 * w;
-      // this warp's operand of dU0 is no longer read: its place stages dV
-      store_tokens(R, own + W::kX + w * 3 * kOperand, a.dvp + (orow * a.Hv + h) * a.dv + row0,
-                   int64_t(a.Hv) * a.dv, n, lane);
-    }
+    // this warp's operand of dU0 is no longer read: its place stages dV
+    const int n = min(kDeltaChunk, len - c * kDeltaChunk) - 16 * w;
+    const int64_t orow = b * a.T + tok0 + int64_t(c) * kDeltaChunk + 16 * w;
+    store_tokens(R, own + W::kX + w * 3 * kOperand, a.dvp + (orow * a.Hv + h) * a.dv + row0, int64_t(a.Hv) * a.dv,
+                 n, lane);
   }
   __syncthreads();
   if (a.dstate_in) store_state<DK>(S, a.dstate_in, srow, w, lane);
@@ -257,10 +224,8 @@ struct KeyGradArgs {
   DeltaMap map;
   float scale;
   const unsigned char* blocks;
-  const unsigned char *snap, *dsnap, *u, *dx;
-  const float *odot, *vdot, *bdot, *sdot;
-  int row_blocks;     // partial sums over rows of dv
-  int ahead;          // CTAs between one and the next on its SM
+  const unsigned char *snap, *dsnap, *e, *dr;
+  int ahead;                     // CTAs between one and the next on its SM
   int64_t block_bytes, gate_at;  // a chunk's block, and the gates in it
   __nv_bfloat16 *dq, *dk;
   float *dg, *dbeta;
@@ -273,98 +238,98 @@ __device__ __forceinline__ void prefetch_bulk(const unsigned char* from, int64_t
 }
 
 constexpr int kKeyThreads = 512;
-constexpr int kPanel = 128;  // dv columns a pass
 
-// Shared memory.  Every operand is tiles of 128-byte rows, swizzled:
-//   dO      [2 blocks of 64 dv][64 tokens, then 64 rows of zeros]
-//   dX, U   [2 parts][up to 128 rows of dv][64 tokens]
-//   states  [2 parts][pieces of 8 dk][up to 128 rows of dv], not swizzled: S,
-//           then dS'
-//   K, Q    [blocks of 64 dk][64 tokens]
-//   P       [2 parts][P1, L][64 rows][64 columns]
+// Shared memory, for a pass over a panel of kPanel rows of dv.  Every operand is tiles
+// of 128-byte rows, swizzled:
+//   dO      [64 tokens, then 64 rows of zeros][dv]
+//   dR, E   [3 parts][rows of dv][64 tokens]
+//   states  [3 parts][pieces of 8 dk][rows of dv], not swizzled: S, then dS'
+//   Q, K    [blocks of 64 dk][64 tokens of Q, then of K]
+//   P       [3 parts][P1, L][64 rows][64 columns]
+// and what dg is summed from.
 struct KeyShape {
   static constexpr uint32_t kSeg = 8192;
-  static constexpr uint32_t kZero = kSeg;  // the zeros below the first block
-  static constexpr uint32_t kX = 4 * kSeg, kU = kX + 32768, kTokPart = 16384;
-  static constexpr uint32_t kState = kU + 32768;
-  static constexpr uint32_t kStatePart = 32768;
-  static constexpr uint32_t kK = kState + 2 * kStatePart;
-  static constexpr uint32_t kQ = kK + 2 * kSeg;
-  static constexpr uint32_t kP = kQ + 2 * kSeg;
-  static constexpr uint32_t kPPart = 2 * kSeg;
-  static constexpr uint32_t kSums = kP + 2 * kPPart;  // G pairs, gates, barriers
-  static constexpr uint32_t kBytes = kSums + 512 + 768 + 64;
+  static constexpr uint32_t kZero = kSeg;  // the zeros below dO
+  static constexpr uint32_t kX = 2 * kSeg, kTokPart = kSeg, kE = kX + 3 * kTokPart;
+  static constexpr uint32_t kState = kE + 3 * kTokPart, kStatePart = 2 * kSeg;
+  static constexpr uint32_t kQ = kState + 3 * kStatePart, kBlock = 2 * kSeg, kK = kQ + kSeg;
+  static constexpr uint32_t kP = kQ + 2 * kBlock, kPPart = 2 * kSeg;
+  static constexpr uint32_t kSums = kP + 3 * kPPart;
+};
+struct KeySums {
+  Pair G[kDeltaChunk];
+  float gate[3][kDeltaChunk];  // e^G, e^{G_63 - G}, beta
+  float a[4][128];             // by quarter of dk: a_i, its part of dq and that of dk
+  float c[4][kDeltaChunk];
+  float b[4][128];             // sums of B_ij over a quarter of the columns
+  float r[4][kDeltaChunk];     // by 32 rows i: sum of B_ij over i >= t > j
+  float d[kKeyThreads / 32];   // <dS', S>
 };
 struct KeyBars {
   uint64_t loaded, loaded_d, done_s, done;
   uint32_t tmem;
   int abort;
 };
-// Columns of tensor memory: [dO; dX] U^T, [dO; dX] S, [0; U] dS', and the sums
-// of P's products over the value heads.
-constexpr uint32_t kTmP = 0, kTmS = 64, kTmD = 192, kTmK = 320;
+// Columns of tensor memory: [dO; dR] E^T, [dO; dR] S, [0; E] dS', the sums of P's
+// products over the value heads, [Q; K] K^T.
+constexpr uint32_t kTmP = 0, kTmS = 64, kTmD = 192, kTmK = 320, kTmQ = 448;
 
-// dbeta and dg of a chunk from the walks' sums over the rows, by one warp, two
-// tokens a lane: dbeta_t = sum dR.E, dg_t = sum over i >= t of (dO.O - dV.V)_i +
-// <dS', S'>.
-__device__ __forceinline__ void row_gradients(const KeyGradArgs& a, int64_t ch, int64_t row, int h, int n, int lane) {
-  const int nsl = a.row_blocks;
-  float2 r = make_float2(0.f, 0.f), db = r;
-#pragma unroll 4
-  for (int w = 0; w < nsl; ++w) {
-    const int64_t at = (ch * nsl + w) * kDeltaChunk + 2 * lane;
-    const float2 o = *reinterpret_cast<const float2*>(a.odot + at), v = *reinterpret_cast<const float2*>(a.vdot + at);
-    const float2 e = *reinterpret_cast<const float2*>(a.bdot + at);
-    r.x += o.x - v.x;
-    r.y += o.y - v.y;
-    db.x += e.x;
-    db.y += e.y;
-  }
-  float sd = 0.f;
-  for (int w = lane; w < 4 * nsl; w += 32) sd += a.sdot[ch * 4 * nsl + w];
+// dg of a chunk and head, by one warp, two tokens a lane.  Sums run from the far end
+// (nothing is subtracted), so small ones keep their digits.
+__device__ __forceinline__ void gate_gradient(const KeySums& s, float* dg, int64_t stride, int n, int lane) {
+  const int t0 = 2 * lane;
+  float a[2], c[2], r[2], d = lane < kKeyThreads / 32 ? s.d[lane] : 0.f;
 #pragma unroll
-  for (int m = 16; m; m >>= 1) sd += __shfl_xor_sync(~0u, sd, m);
-  float sum = r.x + r.y;
+  for (int i = 0; i < 2; ++i) {
+    a[i] = c[i] = r[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      a[i] += s.a[w][t0 + i] + s.a[w][64 + t0 + i];
+      c[i] += s.c[w][t0 + i];
+      r[i] += s.r[w][t0 + i];
+    }
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(~0u, d, m);
+  d *= s.gate[0][63];
+  float after = a[0] + a[1], before = c[0] + c[1];
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const float v = __shfl_down_sync(~0u, sum, m);
-    if (lane + m < 32) sum += v;
+    const float x = __shfl_down_sync(~0u, after, m), y = __shfl_up_sync(~0u, before, m);
+    if (lane + m < 32) after += x;
+    if (lane >= m) before += y;
   }
-  float later = __shfl_down_sync(~0u, sum, 1);
-  if (lane == 31) later = 0.f;
-  later += r.y;
-#pragma unroll
-  for (int i = 1; i >= 0; --i) {
-    if (2 * lane + i >= n) continue;
-    const int64_t at = (row + 2 * lane + i) * a.Hv + h;
-    a.dbeta[at] = i ? db.y : db.x;
-    a.dg[at] = (i ? later : later + r.x) + sd;
-  }
+  after = __shfl_down_sync(~0u, after, 1);
+  before = __shfl_up_sync(~0u, before, 1);
+  if (lane == 31) after = 0.f;
+  if (lane == 0) before = 0.f;
+  if (t0 < n) dg[t0 * stride] = (after + a[1] + a[0]) + before + r[0] + d;
+  if (t0 + 1 < n) dg[(t0 + 1) * stride] = (after + a[1]) + (before + c[0]) + r[1] + d;
 }
 
 // One (chunk, key head), on the tensor cores: 128 accumulator rows, dq's 64
-// tokens above dk's 64.  For each value head that shares the key head, in order:
-//   [dO; dX] U^T -> with the decays P1 (rows of dq) and L (below the diagonal)
-//   [dO; dX] S, [0; U] dS': scaled by row and added in registers
+// tokens above dk's 64.  Once: [Q; K] K^T.  For each value head that shares the key
+// head, in order, with U = b E and dX = b dR:
+//   [dO; dR] E^T -> with the decays and betas P1 (rows of dq) and L (below the
+//     diagonal); its lower diagonal is dbeta; with [Q; K] K^T the B_ij of dg
+//   [dO; dR] S, [0; E] dS': scaled by row and added in registers; dotted with q and k
+//     the a_i and c_j of dg
 //   [P1; L] K + [0; P1^T] Q + [0; L^T] K: added over the heads in tensor memory
 // A transposed left operand is a second group of 64 rows below one of zeros.
-// 128 chunks of 10 key heads, two value heads of 128 x 128 each: 184 us, of which
-// 90 would be the bytes (614 MB, mostly states).  Shared memory holds one pass, so
-// a pass's loads (from L2 by then), products and sums follow one another.
-// Operands that are not bf16 as given have two parts (16 bits), and of each
-// product the three largest terms are kept: the results are rounded to bf16.
+// Operands that are not bf16 as given have three parts, and products of parts p, r
+// are kept for p + r < 3, as in the walks.  128 chunks of 10 key heads, two value heads of
+// 128 x 128 each: 379 us, of which 112 would be the bytes (755 MB, mostly states) and 110
+// the products; a pass's loads, products and sums follow one another.
 template <int DK>
 __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradArgs a) {
   extern __shared__ unsigned char smem_raw[];
   using W = KeyShape;
   constexpr int NB = DK / 64;  // blocks of dk
   constexpr int HC = DK / 4;   // columns a thread
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // an offset: its loads stay shared ones
   const uint32_t sb = smem_u32(smem);
-  Pair* G = reinterpret_cast<Pair*>(smem + W::kSums);
-  float* gate = reinterpret_cast<float*>(G + kDeltaChunk);  // e^G, e^{G_63 - G}, beta
-  KeyBars* bars = reinterpret_cast<KeyBars*>(gate + 3 * kDeltaChunk);
+  KeySums& sums = *reinterpret_cast<KeySums*>(smem + W::kSums);
+  KeyBars* bars = reinterpret_cast<KeyBars*>(smem + W::kSums + sizeof(KeySums));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = (warp & 3) * 32 + lane, quarter = warp >> 2;  // accumulator row, quarter of the columns
   const int tok = row & 63;
@@ -401,16 +366,17 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
     const auto* qp = static_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.sb + t * a.q.st + hk * a.q.sh;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      load_tile<8>(smem + W::kK + i * W::kSeg, kp + 64 * i, a.k.st, n, a.k.vec, tid, kKeyThreads);
-      load_tile<8>(smem + W::kQ + i * W::kSeg, qp + 64 * i, a.q.st, n, a.q.vec, tid, kKeyThreads);
+      load_tile<8>(smem + W::kQ + i * W::kBlock, qp + 64 * i, a.q.st, n, a.q.vec, tid, kKeyThreads);
+      load_tile<8>(smem + W::kK + i * W::kBlock, kp + 64 * i, a.k.st, n, a.k.vec, tid, kKeyThreads);
     }
-    for (int i = tid; i < int(2 * W::kSeg / 16); i += kKeyThreads)
-      *reinterpret_cast<uint4*>(smem + W::kZero + (i / 512) * 2 * W::kSeg + (i % 512) * 16) = make_uint4(0, 0, 0, 0);
+    static_assert(kKeyThreads * 16 == W::kSeg, "one piece of the zeros a thread");
+    *reinterpret_cast<uint4*>(smem + W::kZero + tid * 16) = make_uint4(0, 0, 0, 0);
   }
-  // left operand by rows or transposed; all right operands have their rows along
-  // the sum
+  // left operand by rows or transposed; right operands have their rows along the
+  // sum, but for K in [Q; K] K^T
   constexpr uint32_t id_p = idesc_bf16_f32(128, 64, false, true), id_pt = idesc_bf16_f32(128, 64, true, true);
   constexpr uint32_t id_s = idesc_bf16_f32(128, DK, false, true), id_st = idesc_bf16_f32(128, DK, true, true);
+  constexpr uint32_t id_q = idesc_bf16_f32(128, 64, false, false);
   // low words of descriptors: an operand; one below 64 rows of zeros
   const uint32_t su = __shfl_sync(~0u, sb, 0), tmu = __shfl_sync(~0u, tm, 0);
   const uint32_t zeros = (su + W::kZero) >> 4;
@@ -420,53 +386,67 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   // of the one before run, this CTA's or the last one's on this SM: the loads of a
   // pass fill shared memory, so that nothing else overlaps them.
   auto fetch = [&](int64_t linear, int h_next) {
-    const int64_t c = linear % gridDim.x;
-    const int64_t at = c * a.Hv + h_next;
-    prefetch_bulk(a.snap + (int64_t(a.map.doc_of(int(c))) * a.Hv + at) * snap_bytes(a.dv, DK), state_parts(a.dv, DK, 2));
-    prefetch_bulk(a.dx + at * token_tiles(a.dv), token_tiles(a.dv));
-    prefetch_bulk(a.u + at * token_tiles(a.dv), token_tiles(a.dv));
-    prefetch_bulk(a.dsnap + at * state_parts(a.dv, DK, 2), state_parts(a.dv, DK, 2));
+    const int64_t at = (linear % gridDim.x) * a.Hv + h_next;
+    prefetch_bulk(a.snap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
+    prefetch_bulk(a.dr + at * token_tiles(a.dv), token_tiles(a.dv));
+    prefetch_bulk(a.e + at * token_tiles(a.dv), token_tiles(a.dv));
+    prefetch_bulk(a.dsnap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
   };
   const int64_t here = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, after = here + a.ahead;
   float acc[HC];
 #pragma unroll
   for (int e = 0; e < HC; ++e) acc[e] = 0.f;
+  // this thread's row of [Q; K], 8 columns from `piece` of its quarter, dotted with v
+  auto dot_row = [&](int piece, const float* v) {
+    const int at = quarter * (HC / 8) + piece;
+    const uint4 x = *reinterpret_cast<const uint4*>(smem + W::kQ + (at >> 3) * W::kBlock + tile_at<8>(row, at & 7));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_bf16x2(w[e]);
+      sum += f.x * v[2 * e] + f.y * v[2 * e + 1];
+    }
+    return sum;
+  };
   uint32_t it = 0;  // passes over a panel
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
     const int64_t ch = int64_t(chunk) * a.Hv + h;
     const auto* dop = static_cast<const __nv_bfloat16*>(a.dout.data) + b * a.dout.sb + t * a.dout.st + h * a.dout.sh;
+    float dot = 0.f;  // <dS', S>
     for (int v0 = 0; v0 < a.dv; v0 += kPanel, ++it) {
-      const int width = min(kPanel, a.dv - v0), blocks = (width + 63) / 64;
+      const int width = min(kPanel, a.dv - v0);
       const uint32_t par = it & 1;
       const bool last = v0 + kPanel >= a.dv;
-      const int64_t srow = int64_t(v0) * 128;
       const uint32_t state_bytes = uint32_t(width) * DK * 2;  // one part
       // the states' descriptor: core matrices of 8 rows of dv by 16 bytes of dk,
       // 128 bytes apart along the rows, width * 16 along dk
       const uint32_t state_hi = uint32_t(width) | (1u << 14);
       auto state = [&](int p, int ks) { return lo(W::kState + p * W::kStatePart + ks * 256, 128); };
       if (tid == 0) {
-        const int64_t tiles = ch * token_tiles(a.dv) + srow;
-        const unsigned char* ss = a.snap + ((int64_t(s) + chunk) * a.Hv + h) * snap_bytes(a.dv, DK) + state_parts(v0, DK, 2);
-        mbar_arrive_expect_tx(&bars->loaded, uint32_t(4 * width * 128) + 2 * state_bytes);
-        for (int p = 0; p < 2; ++p) {
-          bulk_load(smem + W::kX + p * W::kTokPart, a.dx + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
-          bulk_load(smem + W::kU + p * W::kTokPart, a.u + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
+        const int64_t tiles = ch * token_tiles(a.dv) + int64_t(v0) * 128;
+        const unsigned char* ss = a.snap + ch * state_parts(a.dv, DK) + state_parts(v0, DK);
+        mbar_arrive_expect_tx(&bars->loaded, uint32_t(6 * width * 128) + 3 * state_bytes);
+        for (int p = 0; p < 3; ++p) {
+          bulk_load(smem + W::kX + p * W::kTokPart, a.dr + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
+          bulk_load(smem + W::kE + p * W::kTokPart, a.e + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
         }
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < 3; ++p)
           bulk_load(smem + W::kState + p * W::kStatePart, ss + p * state_bytes, state_bytes, &bars->loaded);
       }
-      for (int i = tid; i < kDeltaChunk * 8 * blocks; i += kKeyThreads) {
-        const int blk = i >> 9, r = (i >> 3) & 63, p = i & 7;
-        if (blk * 64 + p * 8 >= width) continue;
-        unsigned char* d = smem + blk * 2 * W::kSeg + tile_at<8>(r, p);
-        const __nv_bfloat16* src = dop + v0 + blk * 64 + p * 8 + (r < n ? r * a.dout.st : 0);
-        if (a.dout.vec)
-          cp16(smem_u32(d), src, r < n);
-        else if (r < n)
-          store_piece(d, src);
-        else
-          *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+      {
+        static_assert(kKeyThreads == kDeltaChunk * 8, "one piece of dO a thread");
+        const int r = tid >> 3, p = tid & 7;
+        if (p * 8 < width) {
+          unsigned char* d = smem + tile_at<8>(r, p);
+          const __nv_bfloat16* src = dop + v0 + p * 8 + (r < n ? r * a.dout.st : 0);
+          if (a.dout.vec)
+            cp16(smem_u32(d), src, r < n);
+          else if (r < n)
+            store_piece(d, src);
+          else
+            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+        }
       }
       cp_commit();
       cp_wait<0>();
@@ -475,8 +455,13 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
       __syncthreads();
       if (warp == 0) {
         const uint32_t on = elect_one();
-        wait(&bars->loaded, par);
         tc_fence_after_sync();
+        if (it == 0)
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks)
+            mma_ss(on, tmu + kTmQ, lo(W::kQ + (ks >> 2) * W::kBlock + (ks & 3) * 32),
+                   lo(W::kK + (ks >> 2) * W::kBlock + (ks & 3) * 32), id_q, ks > 0);
+        wait(&bars->loaded, par);
         if (v0 == 0 && lane == 0) {
           if (h + 1 < (hk + 1) * group)
             fetch(here, h + 1);
@@ -484,71 +469,99 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
             fetch(after, int(after / gridDim.x) * group);
         }
         __syncwarp();
-        // small terms first; dO is exact, so it has no second part
+        // small terms first; dO is exact, so it has no other parts
 #pragma unroll 1
-        for (int term = 0; term < 3; ++term) {
-          const uint32_t pa = term == 1, pb = term == 0;
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll 1
+          for (int p = 0; p <= sum; ++p)
 #pragma unroll 2
-          for (int ks = 0; ks < width / 16; ++ks) {
-            const uint32_t dos = lo((ks >> 2) * 2 * W::kSeg + (ks & 3) * 32);
-            const uint32_t bu = lo(W::kU + pb * W::kTokPart + ks * 2048), bs = state(pb, ks);
-            const uint32_t ax = below(W::kX + pa * W::kTokPart + ks * 2048);
-            const bool more = v0 > 0 || term > 0 || ks > 0;
-            if (pa == 0) {
-              mma_ss(on, tmu + kTmP, dos, bu, id_p, more);
-              mma_ss(on, tmu + kTmS, dos, bs, id_s, more, state_hi);
+            for (int ks = 0; ks < width / 16; ++ks) {
+              const uint32_t dos = lo(ks * 32), be = lo(W::kE + (sum - p) * W::kTokPart + ks * 2048);
+              const uint32_t bs = state(sum - p, ks), ax = below(W::kX + p * W::kTokPart + ks * 2048);
+              if (p == 0) {
+                const bool more = v0 > 0 || sum < 2 || ks > 0;
+                mma_ss(on, tmu + kTmP, dos, be, id_p, more);
+                mma_ss(on, tmu + kTmS, dos, bs, id_s, more, state_hi);
+              }
+              mma_ss(on, tmu + kTmP, ax, be, id_pt, 1);
+              mma_ss(on, tmu + kTmS, ax, bs, id_st, 1, state_hi);
             }
-            mma_ss(on, tmu + kTmP, ax, bu, id_pt, 1);
-            mma_ss(on, tmu + kTmS, ax, bs, id_st, 1, state_hi);
-          }
-        }
         commit(on, &bars->done_s);
       } else if (v0 == 0 && warp == 1) {  // meanwhile
         const float* from = reinterpret_cast<const float*>(a.blocks + ch * a.block_bytes + a.gate_at);
 #pragma unroll
-        for (int i = 0; i < 3 * kDeltaChunk; i += 32) gate[i + lane] = from[i + lane];
+        for (int i = 0; i < 3 * kDeltaChunk; i += 32) (&sums.gate[0][0])[i + lane] = from[i + lane];
       } else if (v0 == 0 && warp == 2) {
-        gate_sums(a.g, b, t, h, n, lane, G);
-      } else if (v0 == 0 && warp == 3) {
-        row_gradients(a, ch, b * a.T + t, h, n, lane);
+        gate_sums(a.g, b, t, h, n, lane, sums.G);
       }
       __syncwarp();
+      // this thread's share of S, which dS' will replace
+      auto share = [&](int j, float (&x)[8]) {
+        const unsigned char* at = smem + W::kState + (tid + j * kKeyThreads) * 16;
+        uint32_t w[3][4];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const uint4 u = *reinterpret_cast<const uint4*>(at + p * W::kStatePart);
+          w[p][0] = u.x;
+          w[p][1] = u.y;
+          w[p][2] = u.z;
+          w[p][3] = u.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 hi = unpack_bf16x2(w[0][e]), mid = unpack_bf16x2(w[1][e]), low = unpack_bf16x2(w[2][e]);
+          x[2 * e] = hi.x + (mid.x + low.x);
+          x[2 * e + 1] = hi.y + (mid.y + low.y);
+        }
+      };
+      float S[NB][8];
+      wait(&bars->loaded, par);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (tid + j * kKeyThreads < width * (DK / 8)) share(j, S[j]);
       wait(&bars->done_s, par);
       tc_fence_after_sync();
-      if (tid == 0) {  // S is used up: dS' takes its place
-        const unsigned char* ds = a.dsnap + ch * state_parts(a.dv, DK, 2) + state_parts(v0, DK, 2);
-        mbar_arrive_expect_tx(&bars->loaded_d, 2 * state_bytes);
-        for (int p = 0; p < 2; ++p)
+      __syncthreads();  // S is used up: dS' takes its place; the gates and their sums
+      if (tid == 0) {
+        const unsigned char* ds = a.dsnap + ch * state_parts(a.dv, DK) + state_parts(v0, DK);
+        mbar_arrive_expect_tx(&bars->loaded_d, 3 * state_bytes);
+        for (int p = 0; p < 3; ++p)
           bulk_load(smem + W::kState + p * W::kStatePart, ds + p * state_bytes, state_bytes, &bars->loaded_d);
       }
       __syncwarp();
+      const float eg = sums.gate[0][tok], bt = sums.gate[2][tok];
+      float B[16];
       if (last) {
-        __syncthreads();  // the gates and their sums
         // P1 and L: this thread's row, 16 columns
         float v[16];
         read16(trow + kTmP + 16 * quarter, v);
+        read16(trow + kTmQ + 16 * quarter, B);
+        const Pair g = sums.G[tok];
+        float sum = 0.f;
 #pragma unroll
         for (int piece = 0; piece < 2; ++piece) {
-          uint32_t hi[4], low[4];
+          uint32_t p[4][3];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float x[2];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-              const int c = 16 * quarter + piece * 8 + 2 * e + f;
+              const int i = piece * 8 + 2 * e + f, c = 16 * quarter + i;
+              if (is_k && c == tok && tok < n) a.dbeta[(b * a.T + t + tok) * a.Hv + h] = v[i];  // dR.E
               const bool on = is_k ? c < tok : c <= tok;
-              const float d = on ? decay(G[tok], G[c]) : 0.f;
-              x[f] = on ? (is_k ? -d : a.scale * d) * v[piece * 8 + 2 * e + f] : 0.f;
+              const float d = on ? decay(g, sums.G[c]) * sums.gate[2][c] : 0.f;
+              x[f] = on ? (is_k ? -bt * d : a.scale * d) * v[i] : 0.f;
+              B[i] = c < tok ? x[f] * B[i] : 0.f;
+              sum += B[i];
             }
-            uint32_t p[2];
-            split2<2>(x[0], x[1], p);
-            hi[e] = p[0];
-            low[e] = p[1];
+            split2<3>(x[0], x[1], p[e]);
           }
           unsigned char* to = smem + W::kP + (is_k ? W::kSeg : 0) + tile_at<8>(tok, 2 * quarter + piece);
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(to + W::kPPart) = make_uint4(low[0], low[1], low[2], low[3]);
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            *reinterpret_cast<uint4*>(to + q * W::kPPart) = make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
         }
+        sums.b[quarter][row] = sum;
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncthreads();
@@ -558,52 +571,88 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
         tc_fence_after_sync();
         if (last) {
 #pragma unroll 1
-          for (int p = 1; p >= 0; --p)
+          for (int p = 2; p >= 0; --p)
 #pragma unroll 2
             for (int ks = 0; ks < 4; ++ks) {
               const uint32_t pt = W::kP + p * W::kPPart + ks * 2048;
-              const uint32_t bk = lo(W::kK + ks * 2048, W::kSeg), bq = lo(W::kQ + ks * 2048, W::kSeg);
-              mma_ss(on, tmu + kTmK, lo(W::kP + p * W::kPPart + ks * 32), bk, id_s, h > hk * group || p == 0 || ks > 0);
+              const uint32_t bk = lo(W::kK + ks * 2048, W::kBlock), bq = lo(W::kQ + ks * 2048, W::kBlock);
+              mma_ss(on, tmu + kTmK, lo(W::kP + p * W::kPPart + ks * 32), bk, id_s, h > hk * group || p < 2 || ks > 0);
               mma_ss(on, tmu + kTmK, below(pt), bq, id_st, 1);
               mma_ss(on, tmu + kTmK, below(pt + W::kSeg), bk, id_st, 1);
             }
         }
         wait(&bars->loaded_d, par);
 #pragma unroll 1
-        for (int term = 0; term < 3; ++term) {
-          const uint32_t pa = term == 1, pb = term == 0;
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll 1
+          for (int p = 0; p <= sum; ++p)
 #pragma unroll 2
-          for (int ks = 0; ks < width / 16; ++ks)
-            mma_ss(on, tmu + kTmD, below(W::kU + pa * W::kTokPart + ks * 2048), state(pb, ks), id_st,
-                   v0 > 0 || term > 0 || ks > 0, state_hi);
-        }
+            for (int ks = 0; ks < width / 16; ++ks)
+              mma_ss(on, tmu + kTmD, below(W::kE + p * W::kTokPart + ks * 2048), state(sum - p, ks), id_st,
+                     v0 > 0 || sum < 2 || p > 0 || ks > 0, state_hi);
         commit(on, &bars->done);
       }
       __syncwarp();
       if (last) {
-        const float m = is_k ? -gate[tok] : a.scale * gate[tok];
+        // sum of B_ij over this warp's rows i >= t and the columns j < t
+        float before = 0.f;
+        for (int w = 0; w < quarter; ++w) before += sums.b[w][row];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = B[i];
+          B[i] = 16 * quarter + i <= tok ? before : 0.f;
+          before += x;
+        }
+        store_row_sums(B, sums.r[warp & 3] + 16 * quarter, lane);
+        const float m = is_k ? -eg * bt : a.scale * eg;
+        float part = 0.f;
 #pragma unroll
         for (int c0 = 0; c0 < HC; c0 += 16) {
           float v[16];
           read16(trow + kTmS + quarter * HC + c0, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[c0 + e] += m * v[e];
+          for (int e = 0; e < 16; ++e) {
+            v[e] *= m;
+            acc[c0 + e] += v[e];
+          }
+          part += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
         }
+        sums.a[quarter][row] = part;
       }
+      wait(&bars->loaded_d, par);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (tid + j * kKeyThreads < width * (DK / 8)) {
+          float x[8];
+          share(j, x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot += S[j][e] * x[e];
+        }
       wait(&bars->done, par);
       tc_fence_after_sync();
       if (last) {
-        const float m = gate[kDeltaChunk + tok];
+        const float m = is_k ? sums.gate[1][tok] * bt : 0.f;
+        float part = 0.f;
 #pragma unroll
         for (int c0 = 0; c0 < HC; c0 += 16) {
           float v[16];
           read16(trow + kTmD + quarter * HC + c0, v);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[c0 + e] += is_k ? m * v[e] : 0.f;
+          for (int e = 0; e < 16; ++e) {
+            v[e] = is_k ? m * v[e] : 0.f;
+            acc[c0 + e] += v[e];
+          }
+          part += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
         }
+        if (is_k) sums.c[quarter][tok] = part;
+        #pragma unroll
+        for (int m2 = 16; m2; m2 >>= 1) dot += __shfl_xor_sync(~0u, dot, m2);
+        if (lane == 0) sums.d[warp] = dot;
       }
       tc_fence_before_sync();
       __syncthreads();  // the panel's buffers, and the sums, are free
+      // the sums are next written behind a barrier that this warp joins later
+      if (last && warp == 3) gate_gradient(sums, a.dg + (b * a.T + t) * a.Hv + h, a.Hv, n, lane);
     }
   }
   tc_fence_after_sync();
@@ -641,7 +690,7 @@ cudaError_t run_team_reverse(const LaunchEnv& env, const ReverseArgs& r) {
 
 template <int DK>
 cudaError_t run_key_grad(const LaunchEnv& env, const KeyGradArgs& g) {
-  constexpr int smem = KeyShape::kBytes + 1024;
+  constexpr int smem = KeyShape::kSums + int(sizeof(KeySums) + sizeof(KeyBars)) + 1024;
   const cudaError_t e = cudaFuncSetAttribute(delta_key_grad_kernel<DK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -651,55 +700,43 @@ cudaError_t run_key_grad(const LaunchEnv& env, const KeyGradArgs& g) {
 
 // Scratch after the blocks, in bytes.
 struct GradLayout {
-  size_t snap, dsnap, e, u, dx, odot, vdot, bdot, sdot, total;
+  size_t snap, dsnap, e, dr, total;
 };
-GradLayout grad_layout(int64_t nchunks, int64_t ndocs, int Hv, int dk, int dv) {
+GradLayout grad_layout(int64_t nchunks, int Hv, int dk, int dv) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t heads = size_t(nchunks) * size_t(Hv), dots = heads * (dv / 16) * kDeltaChunk * sizeof(float);
+  const size_t heads = size_t(nchunks) * size_t(Hv);
   GradLayout L;
   size_t at = up(heads * kWideGrad);  // the larger of the blocks' two forms
   auto take = [&](size_t* where, size_t bytes) {
     *where = at;
     at += up(bytes);
   };
-  take(&L.snap, size_t(nchunks + ndocs) * Hv * size_t(snap_bytes(dv, dk)));
-  take(&L.dsnap, heads * size_t(state_parts(dv, dk, 2)));
-  take(&L.e, heads * dv * kDeltaChunk * sizeof(float));
-  take(&L.u, heads * size_t(token_tiles(dv)));
-  take(&L.dx, heads * size_t(token_tiles(dv)));
-  take(&L.odot, dots);
-  take(&L.vdot, dots);
-  take(&L.bdot, dots);
-  take(&L.sdot, heads * (dv / 4) * sizeof(float));
+  take(&L.snap, heads * size_t(state_parts(dv, dk)));
+  take(&L.dsnap, heads * size_t(state_parts(dv, dk)));
+  take(&L.e, heads * size_t(token_tiles(dv)));
+  take(&L.dr, heads * size_t(token_tiles(dv)));
   L.total = at;
   return L;
 }
 
 }  // namespace
 
-size_t delta_grad_scratch(int64_t nchunks, int64_t ndocs, int Hv, int dk, int dv) {
-  return grad_layout(nchunks, ndocs, Hv, dk, dv).total;
-}
+size_t delta_grad_scratch(int64_t nchunks, int Hv, int dk, int dv) { return grad_layout(nchunks, Hv, dk, dv).total; }
 
 cudaError_t launch_delta_grad(const LaunchEnv& env, const DeltaGradArgs& a) {
   const DeltaArgs& f = a.f;
-  const GradLayout L = grad_layout(f.map.nchunks, f.map.ndocs, f.Hv, f.dk, f.dv);
-  auto at = [&](size_t off) { return reinterpret_cast<float*>(f.ws + off); };
+  const GradLayout L = grad_layout(f.map.nchunks, f.Hv, f.dk, f.dv);
   cudaError_t e = cudaSuccess;
   const bool by_head = delta_by_head(f.map.ndocs, f.Hv, f.dv, env.num_sms);
   if (f.map.nchunks > 0 && (e = launch_delta_prepare(env, f, f.ws, true, by_head)) != cudaSuccess) return e;
   DeltaSave save;
-  save.dout = a.dout;
   save.snap = f.ws + L.snap;
-  save.e = at(L.e);
-  save.u = f.ws + L.u;
-  save.odot = at(L.odot);
+  save.e = f.ws + L.e;
   e = by_head ? launch_head_walk(env, f, f.ws, &save) : launch_team_walk(env, f, f.ws, &save);
   if (e != cudaSuccess) return e;
   ReverseArgs r;
   r.q = f.q;
   r.k = f.k;
-  r.v = f.v;
   r.dout = a.dout;
   r.Hk = f.Hk;
   r.Hv = f.Hv;
@@ -709,16 +746,11 @@ cudaError_t launch_delta_grad(const LaunchEnv& env, const DeltaGradArgs& a) {
   r.scale = f.scale;
   r.blocks = f.ws;
   r.status = env.status;
-  r.snap = save.snap;
-  r.e = save.e;
   r.dstate_out = a.dstate_out;
   r.dstate_in = a.dstate_in;
   r.dvp = static_cast<__nv_bfloat16*>(a.dv);
-  r.dx = f.ws + L.dx;
+  r.dr = f.ws + L.dr;
   r.dsnap = f.ws + L.dsnap;
-  r.vdot = at(L.vdot);
-  r.bdot = at(L.bdot);
-  r.sdot = at(L.sdot);
   KeyGradArgs g;
   g.q = f.q;
   g.k = f.k;
@@ -731,21 +763,16 @@ cudaError_t launch_delta_grad(const LaunchEnv& env, const DeltaGradArgs& a) {
   g.map = f.map;
   g.scale = f.scale;
   g.blocks = f.ws;
-  g.snap = r.snap;
+  g.snap = save.snap;
   g.dsnap = r.dsnap;
-  g.u = save.u;
-  g.dx = r.dx;
+  g.e = save.e;
+  g.dr = r.dr;
   g.ahead = env.num_sms;
   g.status = env.status;
-  g.odot = save.odot;
-  g.vdot = r.vdot;
-  g.bdot = r.bdot;
-  g.sdot = r.sdot;
   g.dq = static_cast<__nv_bfloat16*>(a.dq);
   g.dk = static_cast<__nv_bfloat16*>(a.dk);
   g.dg = a.dg;
   g.dbeta = a.dbeta;
-  g.row_blocks = by_head ? (f.dv + 31) / 32 : f.dv / 16;
   g.block_bytes = by_head ? kWideGrad : kBlkGrad;
   g.gate_at = by_head ? kWideGate : kBlkGate;
   if (by_head)

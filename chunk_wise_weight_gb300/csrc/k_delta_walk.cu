@@ -9,11 +9,10 @@
 // then 1000 to 2000 cycles in which the 16 warps read, scale, split and write, at
 // 0.4 to 0.5 instructions a cycle and scheduler.  24001 tokens in 7 documents, 16
 // heads of 64 x 128: 261 us, as long as its longest document, 8100 cycles a chunk;
-// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 330 and 422 us,
-// 10000 and 12700 cycles a chunk (with the states' and E's rows 128 bytes apart in
-// memory 731 and 730 us; with the snapshots stored ahead of the products 45 and 30
-// more; with shared memory read through generic addresses, whose registers then
-// spill, 43 and 20 more).
+// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 277 and 375 us,
+// 8400 and 11300 cycles a chunk (with the snapshots stored ahead of the products some
+// 40 us more; with shared memory read through generic addresses, whose registers then
+// spill, 20 to 40 more).
 #include <algorithm>
 #include <type_traits>
 
@@ -35,9 +34,6 @@ __device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d_tmem, uint32
       "r"(a_tmem), "r"(b_lo), "r"(kHi), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void* from) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(from)) : "memory");
-}
 
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -56,7 +52,8 @@ __device__ __forceinline__ void again(int& a, int& b) { asm volatile("" : "+r"(a
 // 16 numbers of this thread's row as operand columns: NP parts, `part` columns
 // from one to the next.
 template <int NP>
-__device__ __forceinline__ void put16(uint32_t taddr, uint32_t part, const float* v, uint32_t (&r)[NP][8]) {
+__device__ __forceinline__ void put16(uint32_t taddr, uint32_t part, const float* v) {
+  uint32_t r[NP][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t p[NP];
@@ -72,65 +69,36 @@ __device__ __forceinline__ void put16(uint32_t taddr, uint32_t part, const float
                  "r"(r[q][6]), "r"(r[q][7])
                  : "memory");
 }
-template <int NP>
-__device__ __forceinline__ void put16(uint32_t taddr, uint32_t part, const float* v) {
-  uint32_t r[NP][8];
-  put16<NP>(taddr, part, v, r);
-}
 
-// Two neighbouring pieces (16 numbers) of row r, from `piece`, of a tile of
-// 128-byte rows with swizzled pieces, in shared memory.
-__device__ __forceinline__ void stage_pieces(unsigned char* tile, int r, int piece, const uint32_t (&v)[8]) {
-  *reinterpret_cast<uint4*>(tile + tile_at<8>(r, piece)) = make_uint4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<uint4*>(tile + tile_at<8>(r, piece + 1)) = make_uint4(v[4], v[5], v[6], v[7]);
-}
-// A quarter of a row of a state, the first two parts, into a snapshot.
+constexpr int kTokTile = 16384;  // [128 rows of dv][64 tokens] bf16, pieces of 8 swizzled
+
+// A quarter of a row of a state into a snapshot.
 template <int DK>
 __device__ __forceinline__ void snap_parts(unsigned char* snap, int dv, int row, int quarter, const float* S) {
 #pragma unroll
   for (int i = 0; i < DK / 4; i += 8) {
-    uint32_t p[4][2];
+    uint32_t p[4][3];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) split2<2>(S[i + 2 * j], S[i + 2 * j + 1], p[j]);
-    unsigned char* at = snap + piece_at<DK>(dv, row, 2, 0, (quarter * (DK / 4) + i) / 8);
-    *reinterpret_cast<uint4*>(at) = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
-    *reinterpret_cast<uint4*>(at + int64_t(DK / 8) * min(128, dv - (row & ~127)) * 16) =
-        make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
+    for (int j = 0; j < 4; ++j) split2<3>(S[i + 2 * j], S[i + 2 * j + 1], p[j]);
+    unsigned char* at = snap + piece_at<DK>(dv, row, 0, (quarter * (DK / 4) + i) / 8);
+    const int64_t part = int64_t(DK / 8) * min(kPanel, dv - row / kPanel * kPanel) * 16;
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<uint4*>(at + q * part) = make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
   }
 }
-
-// Sums of 16 numbers over the lanes of a warp; lanes 0, 2, .. 30 store them.
-__device__ __forceinline__ void store_row_sums(float (&x)[16], float* to, int lane) {
-  int m = 16;
+// 16 numbers of row r, three parts, as pieces of three tiles of 128 rows.
+__device__ __forceinline__ void stage_parts(unsigned char* tiles, int r, int piece, const float* v) {
 #pragma unroll
-  for (int cnt = 8; cnt >= 1; cnt >>= 1, m >>= 1) {
-    const bool up = lane & m;
+  for (int i = 0; i < 2; ++i) {
+    uint32_t p[4][3];
 #pragma unroll
-    for (int i = 0; i < cnt; ++i) {
-      const float send = up ? x[i] : x[i + cnt], keep = up ? x[i + cnt] : x[i];
-      x[i] = keep + __shfl_xor_sync(~0u, send, m);
-    }
+    for (int j = 0; j < 4; ++j) split2<3>(v[8 * i + 2 * j], v[8 * i + 2 * j + 1], p[j]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<uint4*>(tiles + q * kTokTile + tile_at<8>(r, piece + i)) =
+          make_uint4(p[0][q], p[1][q], p[2][q], p[3][q]);
   }
-  x[0] += __shfl_xor_sync(~0u, x[0], 1);
-  if ((lane & 1) == 0) to[lane >> 1] = x[0];
-}
-// Two such sums side by side.
-__device__ __forceinline__ void store_row_sums(float (&x)[16], float (&y)[16], float* to_x, float* to_y, int lane) {
-  int m = 16;
-#pragma unroll
-  for (int cnt = 8; cnt >= 1; cnt >>= 1, m >>= 1) {
-    const bool up = lane & m;
-#pragma unroll
-    for (int i = 0; i < cnt; ++i) {
-      const float sx = up ? x[i] : x[i + cnt], kx = up ? x[i + cnt] : x[i];
-      const float sy = up ? y[i] : y[i + cnt], ky = up ? y[i + cnt] : y[i];
-      x[i] = kx + __shfl_xor_sync(~0u, sx, m);
-      y[i] = ky + __shfl_xor_sync(~0u, sy, m);
-    }
-  }
-  // lanes 2 i: sum i of x, lanes 2 i + 1: of y
-  const float send = lane & 1 ? x[0] : y[0], keep = lane & 1 ? y[0] : x[0];
-  (lane & 1 ? to_y : to_x)[lane >> 1] = keep + __shfl_xor_sync(~0u, send, 1);
 }
 
 struct TcArgs {
@@ -144,7 +112,7 @@ struct TcArgs {
   bool out_fp32;
   const unsigned char* blocks;
   unsigned int* status;
-  DeltaSave save;  // SAVE only
+  DeltaSave save;  // NO = 0 only
 };
 
 constexpr int kTcWarps = 16;  // compute warps: four threads a row of the state
@@ -203,22 +171,27 @@ struct TcBars {
 // state's update.
 constexpr uint32_t kTmS = 0, kTmW = 0, kTmU = 96, kTmX = 192, kTmO = 192, kTmP = 288, kTmD = 352;
 
-template <int DK, bool SAVE, int NO>
+// Shared memory: two stages of what the products read (K, E map, for the output Q and
+// the scores) and of V and the gates, then what leaves: the output in bf16, or E in
+// three parts.
+template <int DK, int NO>
 struct TcShape {
   static constexpr uint32_t kTile = kDeltaChunk * DK * 2;
-  static constexpr uint32_t kQ = kTile, kE = 2 * kTile, kM = kE + 3 * kWideTile;
+  static constexpr uint32_t kQ = kTile, kE = (NO ? 2 : 1) * kTile, kM = kE + 3 * kWideTile;
   static constexpr uint32_t kTiles = kM + NO * kWideTile;  // what the products read
-  static constexpr uint32_t kV = 0, kDo = kDeltaChunk * 256, kGate = (SAVE ? 2 : 1) * kDo, kRest = kGate + 768;
-  static constexpr uint32_t kOut = 2 * kTiles + 2 * kRest;  // [64 tokens][128] bf16 on its way out
-  static constexpr uint32_t kBars = kOut + (NO == 2 ? kDeltaChunk * 256 : 0);
-  static constexpr int64_t kBlock = SAVE ? kWideGrad : kWideFwd;
+  static constexpr uint32_t kV = 0, kGate = kDeltaChunk * 256, kRest = kGate + 768;
+  static constexpr uint32_t kOut = 2 * kTiles + 2 * kRest;
+  static constexpr uint32_t kBars = kOut + (NO == 0 ? 3 * kTokTile : NO == 2 ? kDeltaChunk * 256 : 0);
+  static constexpr int64_t kBlock = NO ? kWideFwd : kWideGrad;
   static constexpr uint32_t kSmem = kBars + sizeof(TcBars) + 1024;
 };
 
-template <int DK, bool SAVE, int NO>
+// NO: as in delta_walk_kernel.
+template <int DK, int NO>
 __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  using W = TcShape<DK, SAVE, NO>;
+  using W = TcShape<DK, NO>;
+  constexpr bool SAVE = NO == 0;
   constexpr int HS = DK / 4;  // columns of the state a thread
   constexpr uint32_t SP = DK / 2;  // columns of tensor memory a part of the state
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // an offset: its loads stay shared ones
@@ -227,7 +200,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->full[i], 3);
-      mbar_init(&bars->empty[i], kTcWarps + (SAVE ? 2 : 1));
+      mbar_init(&bars->empty[i], kTcWarps + 1);
     }
     uint64_t* ready[] = {&bars->s_ready, &bars->x_ready, &bars->w_ready, &bars->u_ready};
     for (uint64_t* r : ready) mbar_init(r, kTcWarps);
@@ -264,16 +237,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
     const int hk = h / (a.Hv / a.Hk), lw = warp - kTcWarps - 1;  // 0 .. 2
     const int pieces = rows / 8;
     if (lw == 2 && SAVE) {
-      unsigned char* u = a.save.u + (chunk0 * a.Hv + h) * token_tiles(a.dv) + row0 * 128;
-      for (int c = 0; c < nchunks; ++c, u += a.Hv * token_tiles(a.dv)) {
-        const int st = c & 1;
-        wait(&bars->out_ready[st], (c >> 1) & 1);
+      unsigned char* e = a.save.e + (chunk0 * a.Hv + h) * token_tiles(a.dv) + row0 * 128;
+      for (int c = 0; c < nchunks; ++c, e += a.Hv * token_tiles(a.dv)) {
+        wait(&bars->out_ready[c & 1], (c >> 1) & 1);
         if (lane == 0) {
-          bulk_store(u, smem + st * W::kTiles + W::kE, rows * 128);
-          bulk_store(u + int64_t(a.dv) * 128, smem + 2 * W::kTiles + st * W::kRest + W::kV, rows * 128);
+          for (int p = 0; p < 3; ++p) bulk_store(e + int64_t(p) * a.dv * 128, smem + W::kOut + p * kTokTile, rows * 128);
           bulk_commit_group();
           bulk_wait_group_read<0>();
-          mbar_arrive(&bars->empty[st]);
+          mbar_arrive(&bars->out_free);
         }
         __syncwarp();
       }
@@ -288,13 +259,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         if (lane == 0) mbar_arrive(&bars->out_free);
       }
     } else if (lw < 2) {
-      // K and V, Q and dO
+      // K and V, Q; in the gradient's form K, V
+      const bool tiles_here = !SAVE || lw == 0, rows_here = lw == (SAVE ? 1 : 0);
       const HeadView& tv = lw ? a.q : a.k;
       const auto* tile = static_cast<const __nv_bfloat16*>(tv.data) + b * tv.sb + tok0 * tv.st + hk * tv.sh;
-      const HeadView& rv = SAVE && lw ? a.save.dout : a.v;
-      const auto* plain = static_cast<const __nv_bfloat16*>(rv.data) + b * rv.sb + tok0 * rv.st + h * rv.sh + row0;
-      const int64_t tile_st = tv.st, plain_st = rv.st;
-      const bool tile_vec = tv.vec, plain_vec = rv.vec;
+      const auto* plain = static_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + tok0 * a.v.st + h * a.v.sh + row0;
+      const int64_t tile_st = tv.st, plain_st = a.v.st;
+      const bool tile_vec = tv.vec, plain_vec = a.v.vec;
       for (int c = 0; c < nchunks; ++c, tile += kDeltaChunk * tile_st, plain += kDeltaChunk * plain_st) {
         const int st = c & 1, n = min(kDeltaChunk, len - c * kDeltaChunk);
         if (c >= 2) wait(&bars->empty[st], ((c >> 1) & 1) ^ 1);
@@ -307,10 +278,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
           bulk_load(rest + W::kGate, blk + kWideGate, 768, &bars->full[st]);
         }
         __syncwarp();
+        if (tiles_here)
 #pragma unroll
-        for (int i = 0; i < DK / 64; ++i)
-          warp_load_tile<8>(tiles + lw * W::kQ + i * 8192, tile + 64 * i, tile_st, n, tile_vec, lane);
-        if (SAVE || lw == 0) load_rows(rest + (lw ? W::kDo : W::kV), plain, plain_st, pieces, n, plain_vec, lane);
+          for (int i = 0; i < DK / 64; ++i)
+            warp_load_tile<8>(tiles + lw * W::kQ + i * 8192, tile + 64 * i, tile_st, n, tile_vec, lane);
+        if (rows_here) load_rows(rest + W::kV, plain, plain_st, pieces, n, plain_vec, lane);
         cp_wait_all();
         fence_proxy_async_smem();  // K and Q are read by the tensor cores
         __syncwarp();
@@ -353,13 +325,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
           mma_ts(on, tmu + kTmP, tmu + kTmS + p * SP + ks * 8, sk + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_tok,
                  p < 2 || ks > 0);
       commit(on, &bars->p_done);
+      if constexpr (!SAVE) {
 #pragma unroll
-      for (int p = NO - 1; p >= 0; --p)
+        for (int p = NO - 1; p >= 0; --p)
 #pragma unroll
-        for (int ks = 0; ks < DK / 16; ++ks)
-          mma_ts(on, tmu + kTmD, tmu + kTmS + p * SP + ks * 8,
-                 sk + ((W::kQ + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_tok, p < NO - 1 || ks > 0);
-      commit(on, &bars->q_done);
+          for (int ks = 0; ks < DK / 16; ++ks)
+            mma_ts(on, tmu + kTmD, tmu + kTmS + p * SP + ks * 8,
+                   sk + ((W::kQ + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_tok, p < NO - 1 || ks > 0);
+        commit(on, &bars->q_done);
+      }
       wait(&bars->x_ready, par);
       tc_fence_after_sync();
       map(tmu + kTmP, tmu + kTmX, sk + (W::kE >> 4), std::integral_constant<int, 3>());
@@ -372,10 +346,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         for (int ks = 0; ks < 4; ++ks)
           mma_ts(on, tmu + kTmD, tmu + kTmW + p * 32 + ks * 8, sk + lbo + ((ks * 2048) >> 4), id_state, p < 2 || ks > 0);
       commit(on, &bars->d_done);
-      wait(&bars->u_ready, par);
-      tc_fence_after_sync();
-      map(tmu + kTmO, tmu + kTmU, sk + (W::kM >> 4), std::integral_constant<int, NO>());
-      commit(on, &bars->m_done);
+      if constexpr (!SAVE) {
+        wait(&bars->u_ready, par);
+        tc_fence_after_sync();
+        map(tmu + kTmO, tmu + kTmU, sk + (W::kM >> 4), std::integral_constant<int, NO>());
+        commit(on, &bars->m_done);
+      }
       commit(on, &bars->empty[st]);
     }
     __syncwarp();
@@ -415,33 +391,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[i + e] = last * S[i + e] + v[e];
       }
-      wait(&bars->m_done, c & 1);
-      tc_fence_after_sync();
-      float v[kTok];
-      read16(trow + kTmO + kTok * quarter, v);
+      if constexpr (!SAVE) {
+        wait(&bars->m_done, c & 1);
+        tc_fence_after_sync();
+        float v[kTok];
+        read16(trow + kTmO + kTok * quarter, v);
 #pragma unroll
-      for (int e = 0; e < kTok; ++e) O[e] += v[e];
+        for (int e = 0; e < kTok; ++e) O[e] += v[e];
+      }
     };
     auto finish_out = [&](int c) {
-      if constexpr (SAVE) {
-        // dO.O over the warp's 32 rows
-        const unsigned char* col = smem + 2 * W::kTiles + (c & 1) * W::kRest + W::kDo + kTok * quarter * 256 + row * 2;
-#pragma unroll
-        for (int e = 0; e < kTok; ++e)
-          O[e] *= active ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(col + e * 256)) : 0.f;
-        if ((row & ~31) < rows)
-          store_row_sums(O, a.save.odot + (((chunk0 + c) * a.Hv + h) * ((a.dv + 31) / 32) + (row0 + row) / 32) * kDeltaChunk + kTok * quarter,
-                         lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->empty[c & 1]);
-      } else if constexpr (NO == 2) {
+      if constexpr (NO == 2) {
         if (c > 0) wait(&bars->out_free, (c - 1) & 1);
         unsigned char* to = smem + W::kOut + kTok * quarter * 256 + row * 2;
 #pragma unroll
         for (int e = 0; e < kTok; ++e) *reinterpret_cast<__nv_bfloat16*>(to + e * 256) = __float2bfloat16_rn(O[e]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->out_ready[c & 1]);
-      } else {
+      } else if constexpr (NO == 3) {
         const int n = min(kDeltaChunk, len - c * kDeltaChunk) - kTok * quarter;
         float* out = static_cast<float*>(a.out) +
                      ((b * a.T + tok0 + int64_t(c) * kDeltaChunk + kTok * quarter) * a.Hv + h) * a.dv + row0 + row;
@@ -461,15 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
     // long as the operand (between put and arrive they cost every chunk 2000 cycles)
     auto snap_s = [&](int c) {
       if (active)
-        snap_parts<DK>(a.save.snap + ((s + chunk0 + c) * a.Hv + h) * snap_bytes(a.dv, DK), a.dv, row0 + row, quarter, S);
-    };
-    auto store_s = [&](int c) {
-      float4* snap = reinterpret_cast<float4*>(a.save.snap + ((s + chunk0 + c) * a.Hv + h) * snap_bytes(a.dv, DK) +
-                                               state_parts(a.dv, DK, 2)) +
-                     int64_t(quarter * (HS / 4)) * a.dv + row0 + row;
-      if (active)
-#pragma unroll
-        for (int i = 0; i < HS; i += 4) snap[int64_t(i / 4) * a.dv] = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        snap_parts<DK>(a.save.snap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK), a.dv, row0 + row, quarter, S);
     };
     for (int c = 0; c < nchunks; ++c) {
       const int st = c & 1;
@@ -501,18 +460,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       }
       put16<3>(trow + kTmX + kTok / 2 * quarter, 32, x);
       arrive(&bars->x_ready);
-      if constexpr (SAVE) store_s(c);
-      wait(&bars->q_done, par);
-      tc_fence_after_sync();
-      read16(trow + kTmD + kTok * quarter, O);
+      if constexpr (!SAVE) {
+        wait(&bars->q_done, par);
+        tc_fence_after_sync();
+        read16(trow + kTmD + kTok * quarter, O);
+#pragma unroll
+        for (int e = 0; e < kTok; e += 4) {
+          const float4 eg = gate[e / 4];
+          O[e] *= a.scale * eg.x;
+          O[e + 1] *= a.scale * eg.y;
+          O[e + 2] *= a.scale * eg.z;
+          O[e + 3] *= a.scale * eg.w;
+        }
+      }
       float ge[kTok];
 #pragma unroll
       for (int e = 0; e < kTok; e += 4) {
-        const float4 eg = gate[e / 4], g2 = gate[16 + e / 4];
-        O[e] *= a.scale * eg.x;
-        O[e + 1] *= a.scale * eg.y;
-        O[e + 2] *= a.scale * eg.z;
-        O[e + 3] *= a.scale * eg.w;
+        const float4 g2 = gate[16 + e / 4];
         ge[e] = g2.x;
         ge[e + 1] = g2.y;
         ge[e + 2] = g2.z;
@@ -534,31 +498,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       put16<3>(trow + kTmW + kTok / 2 * quarter, 32, ge);
       arrive(&bars->w_ready);
       if constexpr (SAVE) {
-        float4* e = reinterpret_cast<float4*>(a.save.e + ((chunk0 + c) * a.Hv + h) * a.dv * kDeltaChunk) +
-                    int64_t(quarter * 4) * a.dv + row0 + row;
-        if (active)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[int64_t(i) * a.dv] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-      }
-#pragma unroll
-      for (int e = 0; e < kTok; e += 4) {
-        const float4 be = gate[32 + e / 4];
-        x[e] *= be.x;
-        x[e + 1] *= be.y;
-        x[e + 2] *= be.z;
-        x[e + 3] *= be.w;
-      }
-      uint32_t ur[NO][8];
-      put16<NO>(trow + kTmU + kTok / 2 * quarter, 32, x, ur);
-      arrive(&bars->u_ready);
-      if constexpr (SAVE) {
-        // U's parts leave from the places of the map and of V, which are used up
-        stage_pieces(smem + st * W::kTiles + W::kE, row, 2 * quarter, ur[0]);
-        stage_pieces(smem + 2 * W::kTiles + st * W::kRest + W::kV, row, 2 * quarter, ur[1]);
+        if (lane == 0) mbar_arrive(&bars->empty[st]);  // V and the gates are read
+        // E's parts leave
+        if (c > 0) wait(&bars->out_free, (c - 1) & 1);
+        stage_parts(smem + W::kOut, row, 2 * quarter, x);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->out_ready[st]);
       } else {
+#pragma unroll
+        for (int e = 0; e < kTok; e += 4) {
+          const float4 be = gate[32 + e / 4];
+          x[e] *= be.x;
+          x[e + 1] *= be.y;
+          x[e + 2] *= be.z;
+          x[e + 3] *= be.w;
+        }
+        put16<NO>(trow + kTmU + kTok / 2 * quarter, 32, x);
+        arrive(&bars->u_ready);
         if (lane == 0) mbar_arrive(&bars->empty[st]);  // V and the gates are read
       }
     }
@@ -566,7 +523,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       finish_state(nchunks - 1);
       finish_out(nchunks - 1);
     }
-    if constexpr (SAVE) store_s(nchunks);
     if (active && a.state_out)
 #pragma unroll
       for (int i = 0; i < HS; i += 4)
@@ -579,8 +535,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
 }
 
 // ------------------------------------------------------------------ reverse
-// Shared memory: two stages of what the products read (K, Q, scores, R map, dO)
-// and of V, in whose place dV leaves, and the gates.
+// Shared memory: two stages of what the products read (K, Q, scores, R map, dO; dR's
+// parts leave from the place of the scores and the map), of dV on its way out, and of
+// the gates.
 template <int DK>
 struct BackShape {
   static constexpr uint32_t kTile = kDeltaChunk * DK * 2;
@@ -647,9 +604,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       for (int it = 0; it < nchunks; ++it, out -= kDeltaChunk * step) {
         const int c = nchunks - 1 - it, st = it & 1;
         wait(&bars->out_ready[st], (it >> 1) & 1);
-        if (lane < 2)
-          bulk_store(a.dx + ((chunk0 + c) * a.Hv + h) * token_tiles(a.dv) + (int64_t(lane) * a.dv + row0) * 128,
-                     smem + st * W::kTiles + W::kM + lane * 16384, rows * 128);
+        if (lane < 3)
+          bulk_store(a.dr + ((chunk0 + c) * a.Hv + h) * token_tiles(a.dv) + (int64_t(lane) * a.dv + row0) * 128,
+                     smem + st * W::kTiles + W::kM + lane * kTokTile, rows * 128);
         bulk_commit_group();
         store_rows(out, step, smem + 2 * W::kTiles + st * W::kRest + W::kV, pieces,
                    min(kDeltaChunk, len - c * kDeltaChunk), lane);
@@ -659,11 +616,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       }
       bulk_wait_group_all();
     } else {
-      // K, V and half of dO; Q and the other half
+      // K and half of dO; Q and the other half
       const HeadView& tv = lw ? a.q : a.k;
       const int64_t t = tok0 + int64_t(nchunks - 1) * kDeltaChunk;
       const auto* tile = static_cast<const __nv_bfloat16*>(tv.data) + b * tv.sb + t * tv.st + hk * tv.sh;
-      const auto* vp = static_cast<const __nv_bfloat16*>(a.v.data) + b * a.v.sb + t * a.v.st + h * a.v.sh + row0;
       const auto* dop = static_cast<const __nv_bfloat16*>(a.dout.data) + b * a.dout.sb + t * a.dout.st + h * a.dout.sh +
                         row0 + 64 * lw;
       const int64_t tile_st = tv.st;
@@ -687,22 +643,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
         // dO as a left operand: rows along the sum over tokens; columns past the
         // head's are zero
         warp_load_tile<8>(tiles + W::kDo + lw * kWideTile, dop, a.dout.st, n, a.dout.vec, lane, pieces - 8 * lw);
-        if (lw == 0) {
-          load_rows(rest + W::kV, vp, a.v.st, pieces, n, a.v.vec, lane);
-        } else {
-          // S' and E, which the rows' threads read themselves, come as far as L2
-          const unsigned char* s1 = a.snap + ((s + chunk0 + c + 1) * a.Hv + h) * snap_bytes(a.dv, DK) + state_parts(a.dv, DK, 2);
-          const unsigned char* e = reinterpret_cast<const unsigned char*>(a.e) + ((chunk0 + c) * a.Hv + h) * a.dv * kDeltaChunk * 4;
-          for (int at = (lane & 15) * 128; at < rows * 16; at += 16 * 128)
-            for (int i = lane >> 4; i < (DK + kDeltaChunk) / 4; i += 2)
-              prefetch_l2((i < DK / 4 ? s1 + int64_t(i) * a.dv * 16 : e + int64_t(i - DK / 4) * a.dv * 16) + row0 * 16 + at);
-        }
         cp_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->full[st]);
         tile -= kDeltaChunk * tile_st;
-        vp -= kDeltaChunk * a.v.st;
         dop -= kDeltaChunk * a.dout.st;
       }
     }
@@ -773,9 +718,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
   } else if (warp < kTcWarps) {
     more_registers<kTcMore>();
     int row = (warp & 3) * 32 + lane, quarter = warp >> 2;
-    const bool active = row < rows, some = (row & ~31) < rows;
+    const bool active = row < rows;
     const uint32_t trow = tm + (uint32_t((warp & 3) * 32) << 16);
-    const int row_blocks = (a.dv + 31) / 32, block = (row0 + row) / 32;
     float S[HS];  // dS'
     const int64_t srow = ((int64_t(s) * a.Hv + h) * a.dv + row0 + row) * DK + quarter * HS;
 #pragma unroll
@@ -801,29 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
 #pragma unroll
       for (int i = 0; i < HS; i += 16) put16<3>(trow + kTmS + (quarter * HS + i) / 2, SP, S + i);
       arrive(&bars->s_ready);
-      // <dS', S'>, this thread's columns
-      {
-        const float4* s1 = reinterpret_cast<const float4*>(
-            a.snap + ((s + chunk0 + c + 1) * a.Hv + h) * snap_bytes(a.dv, DK) + state_parts(a.dv, DK, 2)) +
-            int64_t(quarter * (HS / 4)) * a.dv + row0 + row;
-        float dot = 0.f;
-#pragma unroll
-        for (int first = 0; first < HS / 4; first += HS / 8) {  // (all at once: registers spill)
-          float4 v[HS / 8];
-#pragma unroll
-          for (int i = 0; i < HS / 8; ++i)
-            v[i] = active ? __ldcs(s1 + int64_t(first + i) * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < HS / 8; ++i) {
-            const float* t = S + 4 * (first + i);
-            dot += (v[i].x * t[0] + v[i].y * t[1]) + (v[i].z * t[2] + v[i].w * t[3]);
-          }
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
-        if (lane == 0 && some) a.sdot[(ch * row_blocks + block) * 4 + quarter] = dot;
-      }
-      if (active) snap_parts<DK>(a.dsnap + ch * state_parts(a.dv, DK, 2), a.dv, row0 + row, quarter, S);
+      if (active) snap_parts<DK>(a.dsnap + ch * state_parts(a.dv, DK), a.dv, row0 + row, quarter, S);
       unsigned char* tiles = smem + st * W::kTiles;
       unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
       const float4* gate = reinterpret_cast<const float4*>(rest + W::kGate) + quarter * (kTok / 4);
@@ -870,20 +792,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       put16<3>(trow + kTmY + kTok / 2 * quarter, 32, y);
       arrive(&bars->u_ready);
       const float last = reinterpret_cast<const float*>(rest + W::kGate)[63];
-      {
-        const float4* ep = reinterpret_cast<const float4*>(a.e + ch * a.dv * kDeltaChunk) + int64_t(quarter * 4) * a.dv + row0 + row;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 v = active ? __ldcs(ep + int64_t(i) * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
-          y[4 * i] = v.x;
-          y[4 * i + 1] = v.y;
-          y[4 * i + 2] = v.z;
-          y[4 * i + 3] = v.w;
-        }
-      }
       wait(&bars->e_done, par);
       tc_fence_after_sync();
-      // dR; -e^G dX, dX = b dR; dR.E
+      // dR; -e^G dX, dX = dV = b dR
       read16(trow + kTmP + kTok * quarter, x);
 #pragma unroll
       for (int e = 0; e < kTok; e += 4) {
@@ -895,48 +806,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       }
       put16<3>(trow + kTmW + kTok / 2 * quarter, 32, eg);
       arrive(&bars->w_ready);
+      stage_parts(tiles + W::kM, row, 2 * quarter, x);
+      unsigned char* col = rest + W::kV + kTok * quarter * 256 + row * 2;
 #pragma unroll
       for (int e = 0; e < kTok; e += 4) {
         const float4 be = gate[32 + e / 4];
-        y[e] *= x[e];
-        y[e + 1] *= x[e + 1];
-        y[e + 2] *= x[e + 2];
-        y[e + 3] *= x[e + 3];
-        x[e] *= be.x;
-        x[e + 1] *= be.y;
-        x[e + 2] *= be.z;
-        x[e + 3] *= be.w;
+        const float bx[4] = {be.x * x[e], be.y * x[e + 1], be.z * x[e + 2], be.w * x[e + 3]};
+#pragma unroll
+        for (int f = 0; f < 4; ++f) *reinterpret_cast<__nv_bfloat16*>(col + (e + f) * 256) = __float2bfloat16_rn(bx[f]);
       }
-      // V while dX's parts go to where the scores and the map were, dV to V's place
-      unsigned char* col = rest + W::kV + kTok * quarter * 256 + row * 2;
-      uint32_t vals[kTok / 2];
-#pragma unroll
-      for (int e = 0; e < kTok; e += 2)
-        vals[e / 2] = *reinterpret_cast<const unsigned short*>(col + e * 256) |
-                      uint32_t(*reinterpret_cast<const unsigned short*>(col + e * 256 + 256)) << 16;
-#pragma unroll
-      for (int piece = 0; piece < 2; ++piece) {
-        uint32_t p[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split2<2>(x[8 * piece + 2 * i], x[8 * piece + 2 * i + 1], p[i]);
-        unsigned char* to = tiles + W::kM + tile_at<8>(row, 2 * quarter + piece);
-        *reinterpret_cast<uint4*>(to) = make_uint4(p[0][0], p[1][0], p[2][0], p[3][0]);
-        *reinterpret_cast<uint4*>(to + 16384) = make_uint4(p[0][1], p[1][1], p[2][1], p[3][1]);
-      }
-#pragma unroll
-      for (int e = 0; e < kTok; ++e) *reinterpret_cast<__nv_bfloat16*>(col + e * 256) = __float2bfloat16_rn(x[e]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->out_ready[st]);
-      // dR.E and dV.V over the rows
-#pragma unroll
-      for (int e = 0; e < kTok; e += 2) {
-        const float2 v = unpack_bf16x2(vals[e / 2]);
-        x[e] = active ? x[e] * v.x : 0.f;
-        x[e + 1] = active ? x[e + 1] * v.y : 0.f;
-      }
-      const int64_t at = (ch * row_blocks + block) * kDeltaChunk + kTok * quarter;
-      if (some) store_row_sums(y, x, a.bdot + at, a.vdot + at, lane);
       if (lane == 0) mbar_arrive(&bars->empty[st]);
       wait(&bars->d_done, par);
       tc_fence_after_sync();
@@ -966,9 +847,9 @@ cudaError_t run_head(const LaunchEnv& env, K kernel, uint32_t smem, const A& a) 
   return launch_pdl(kernel, dim3(unsigned(a.map.ndocs * a.Hv * ((a.dv + 127) / 128))), dim3(kTcThreads), smem,
                     env.stream, a);
 }
-template <int DK, bool SAVE, int NO>
+template <int DK, int NO>
 cudaError_t run_head_walk(const LaunchEnv& env, const TcArgs& a) {
-  return run_head(env, head_walk_kernel<DK, SAVE, NO>, TcShape<DK, SAVE, NO>::kSmem, a);
+  return run_head(env, head_walk_kernel<DK, NO>, TcShape<DK, NO>::kSmem, a);
 }
 
 }  // namespace
@@ -993,10 +874,10 @@ cudaError_t launch_head_walk(const LaunchEnv& env, const DeltaArgs& f, const uns
   a.status = env.status;
   if (save) {
     a.save = *save;
-    return f.dk == 64 ? run_head_walk<64, true, 3>(env, a) : run_head_walk<128, true, 3>(env, a);
+    return f.dk == 64 ? run_head_walk<64, 0>(env, a) : run_head_walk<128, 0>(env, a);
   }
-  if (f.out_fp32) return f.dk == 64 ? run_head_walk<64, false, 3>(env, a) : run_head_walk<128, false, 3>(env, a);
-  return f.dk == 64 ? run_head_walk<64, false, 2>(env, a) : run_head_walk<128, false, 2>(env, a);
+  if (f.out_fp32) return f.dk == 64 ? run_head_walk<64, 3>(env, a) : run_head_walk<128, 3>(env, a);
+  return f.dk == 64 ? run_head_walk<64, 2>(env, a) : run_head_walk<128, 2>(env, a);
 }
 
 cudaError_t launch_head_reverse(const LaunchEnv& env, const ReverseArgs& r, int dk) {

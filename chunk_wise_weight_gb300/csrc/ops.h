@@ -162,7 +162,7 @@ struct DeltaGradArgs {
   void *dq, *dk, *dv;       // dense bf16
   float *dg, *dbeta;        // dense fp32 [B, T, Hv]
 };
-size_t delta_grad_scratch(int64_t nchunks, int64_t ndocs, int Hv, int dk, int dv);
+size_t delta_grad_scratch(int64_t nchunks, int Hv, int dk, int dv);
 cudaError_t launch_delta_grad(const LaunchEnv& env, const DeltaGradArgs& a);
 
 // Token by token, one warp a few rows of the state: any type; no scratch.

@@ -390,7 +390,7 @@ size_t ittt_delta_grad_workspace_bytes(int64_t B, int64_t T, int64_t Hv, int64_t
   }
   const int64_t chunks = num_docs > 0 ? T / 64 + num_docs : B * ((T + 63) / 64);
   return table_bytes(num_docs) +
-         ittt::delta_grad_scratch(chunks, num_docs > 0 ? num_docs : B, int(Hv), int(dk), int(dv));
+         ittt::delta_grad_scratch(chunks, int(Hv), int(dk), int(dv));
 }
 
 ittt_status ittt_delta_rule_grad(const ittt_tensor* q, const ittt_tensor* k, const ittt_tensor* v,
@@ -435,7 +435,7 @@ ittt_status ittt_delta_rule_grad(const ittt_tensor* q, const ittt_tensor* k, con
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t table = table_bytes(o.cu_seqlens ? o.num_docs : 0);
   ittt::HostScratch ws;
-  if ((s = ws.take(table + ittt::delta_grad_scratch(d.nchunks, d.S, f.Hv, f.dk, f.dv), o.workspace,
+  if ((s = ws.take(table + ittt::delta_grad_scratch(d.nchunks, f.Hv, f.dk, f.dv), o.workspace,
                    o.workspace_bytes, st)))
     return s;
   ittt::LaunchEnv env;

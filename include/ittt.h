@@ -525,7 +525,10 @@ ITTT_API size_t ittt_delta_workspace_bytes(int64_t B, int64_t T, int64_t Hv, int
  * is run again from state_in): grad_q, grad_k [B,T,Hk,dk] and grad_v
  * [B,T,Hv,dv] bf16, grad_g and grad_beta fp32 [B,T,Hv], all dense.  A key
  * head that several value heads share receives the sum of theirs, formed in
- * fp32 in the order of the heads.  Equal calls give equal bits.
+ * fp32 in the order of the heads.  Equal calls give equal bits.  grad_g of a
+ * token is exact relative to the token's own decay e^{g_t}, however strong
+ * (about 2^-17 of e^{g_t} times the size of the gradient at that factor in its
+ * head), and zero where the decay is.
  */
 typedef struct {
   const ittt_tensor* state_in;       /* as in the forward call */

@@ -91,3 +91,58 @@ def test_slices_in_pairs_packed(cuda_device):
     assert 4 * Hv * 4 > sms and not by_head(4, Hv, dv)
     x, S0, dS1, do = inputs(1, 4, cu[-1], Hv // 2, Hv, 128, dv)
     both(x, S0, dS1, do, cu)
+
+
+# heads that forget within a token beside heads that keep thousands
+DECAYS = (-1e-3, -0.1, -1.0, -3.0, -5.0, -8.0, -12.0, -16.0)
+
+
+def check_gate_gradient(got, ref, g):
+    """grad_g by token and head.  grad_g = e^g z, z the gradient at the factor e^g itself;
+    every term of grad_g carries that factor, so its error is relative to e^g and to the
+    size that z has in the head: products of 24-bit operands, sums of 128 terms whose
+    magnitudes add up to some 11 times the sum (2^-24 * sqrt(128) * 11 = 2^-17), four such
+    chained, taken at 2^-14."""
+    a = torch.exp(g.double())
+    z = torch.where(a > 0, ref / a, 0.0)
+    size = (z ** 2).mean(dim=(0, 1), keepdim=True).sqrt()
+    err = (got.double() - ref).abs()
+    bound = 2.0 ** -14 * a * (z.abs() + size)
+    # below fp32's normal numbers the decays themselves have fewer bits
+    assert torch.all(err <= bound + 1e-35), float((err / (bound + 1e-35)).max())
+
+
+@pytest.mark.parametrize("B,dk,dv", [(1, 128, 64), (2, 64, 128), (8, 128, 96), (8, 64, 144)])
+def test_gate_gradient_of_every_token(cuda_device, B, dk, dv):
+    T, Hv = 150, len(DECAYS)
+    assert by_head(B, Hv, dv) == (B == 8)
+    x, S0, dS1, do = inputs(B, B, T, Hv // 2, Hv, dk, dv)
+    x["g"] = torch.tensor(DECAYS, device="cuda") * (0.8 + 0.4 * torch.rand(B, T, Hv, device="cuda"))
+    x["g"][:, 70:75, :3] = -15.0         # strong tokens in heads that keep
+    x["g"][:, 100, :6] = -60.0
+    x["g"][:, 20, ::2] = -float("inf")   # resets
+    x["g"][:, 64, 1::2] = -2000.0
+    x["beta"][:, 30:33] = 0.0
+    # the definition's exp has no gradient at -inf: a decay of e^-2000 is as much zero
+    y = dict(x, g=torch.where(x["g"] < -1000, torch.full_like(x["g"], -2000.0), x["g"]))
+    ref = grad.reference(y, dk ** -0.5, S0, do, dS1)
+    dS0 = torch.empty_like(S0)
+    got = grad.call(x, do, state_in=S0, grad_state_out=dS1, grad_state_in=dS0)
+    grad.check((*got, dS0), ref)
+    check_gate_gradient(got[3], ref[3], y["g"])
+    assert torch.all(got[3][:, 20, ::2] == 0) and torch.all(got[3][:, 64, 1::2] == 0)
+    # and the differences of the definition, each head's gates along one direction
+    h, S64 = 1e-4, S0.double()
+    way = torch.sign(torch.randn(Hv, device="cuda").double())
+    args = [y[n].double() for n in ("q", "k", "v", "g", "beta")]
+    spans = [(b, 0, T) for b in range(B)]
+
+    def loss(shift):
+        out, S1 = grad.forward64(*args[:3], args[3] + shift * way, args[4], dk ** -0.5, S64, spans)
+        return (out * do.double()).sum((0, 1, 3)) + (S1 * dS1.double()).sum((0, 2, 3))
+
+    slope = (loss(h) - loss(-h)) / (2 * h)  # heads do not meet: one slope each
+    mine = (got[3].double() * way).sum((0, 1))
+    size = got[3].double().abs().sum((0, 1))
+    # the difference's own error: h^2 / 6 of the third derivative, and 1e-16 of the loss / h
+    assert torch.all((slope - mine).abs() <= 2.0 ** -12 * size + 1e-8), (slope, mine)
