@@ -410,6 +410,31 @@ __device__ __forceinline__ void map_tokens(const unsigned char* x, const uint32_
   sum_parts<NP>(t, Y);
 }
 
+// Y += this warp's 16 tokens of X map^T, with the map's blocks read as they are met
+// (off the chain: held from before a barrier they would only cost registers).
+__device__ __forceinline__ void add_map_tokens(const unsigned char* x, uint32_t map, int w, int lane, float (&Y)[2][4]) {
+  float t[3][2][4];  // by p + r
+#pragma unroll
+  for (int p = 0; p < 3; ++p) zero(t[p]);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks)
+    if (ks <= w) {
+      uint32_t xa[3][4], b[3][4];
+#pragma unroll
+      for (int r = 0; r < 3; ++r) ldsm4(b[r], map + r * kImage + image_block(w, 0) + ks * 512 + block_nk(lane));
+#pragma unroll
+      for (int p = 0; p < 3; ++p) get_operand(xa[p], x + (ks * 3 + p) * kOperand, lane);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int r = 0; p + r < 3; ++r) mma2(t[p + r][0], t[p + r][1], xa[p], b[r]);
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Y[i][e] += t[0][i][e] + (t[1][i][e] + t[2][i][e]);
+}
+
 // This warp's dk columns of the rows of a tile, as right operands of W rows.
 template <int DK>
 __device__ __forceinline__ void load_rows(uint32_t (&b)[4][DK / 64][4], uint32_t rows, int w, int lane) {

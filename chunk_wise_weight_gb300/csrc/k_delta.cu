@@ -11,10 +11,13 @@
 // The inverse and M depend on q, k, g and b alone: a first kernel forms them
 // for all chunks at once.  The second walks the chunks in order.
 //
-// 8192 tokens, 20 heads of 128 x 128 (10 key heads): 48 + 399 us.  The call's bytes
+// 8192 tokens, 20 heads of 128 x 128 (10 key heads): 48 + 434 us.  The call's bytes
 // would pass in 19 us and its products in 10; it is bound by the chain of 128
-// chunks, 3.1 us each, of three products that wait for one another (token by token
-// it would be 8192 steps of 0.9 us).
+// chunks, 3.4 us each, of three products that wait for one another (token by token
+// it would be 8192 steps of 0.9 us).  The output's products have 24-bit operands too,
+// so that a bf16 output is the exact one's rounding; with 16 bits, which moved 0.3% of
+// the outputs to the other neighbour, the walk took 398 us (heads of 64 x 64: 4096
+// tokens of 16 heads 183 us then, 147 now, with the scores read where they are used).
 #include <algorithm>
 
 #include "delta.cuh"
@@ -280,22 +283,22 @@ struct WalkArgs {
   bool out_fp32;
   const unsigned char* blocks;
   unsigned int* status;
-  DeltaSave save;  // NO = 0 only
+  DeltaSave save;  // SAVE only
 };
 
 // Shared memory of a CTA of `ns` slices: two stages (K, E map, gates, V, and for the
 // output Q and the scores), then what each slice's warps exchange.
-template <int DK, int NO>
+template <int DK, bool SAVE>
 struct WalkShape {
   static constexpr int kTile = kDeltaChunk * DK * 2;
-  static constexpr int kMap = (NO ? 2 : 1) * kTile;
-  static constexpr int kMaps = (3 + NO) * kImage;
+  static constexpr int kMap = (SAVE ? 1 : 2) * kTile;
+  static constexpr int kMaps = (SAVE ? 3 : 6) * kImage;
   static constexpr int kGate = kMap + kMaps;
   static constexpr int kCols = kGate + 1024;
   static constexpr int kX = DK / 16 * 3 * kOperand;  // operands of X, after the state's
   static constexpr int kW = kX + 12 * kOperand;      // of e^{G_63 - G} U
   static constexpr int kU = kW + 12 * kOperand;      // of U
-  static constexpr int kOwn = kU + 4 * NO * kOperand;
+  static constexpr int kOwn = kU + (SAVE ? 0 : 12 * kOperand);
   static __host__ __device__ constexpr int stage(int ns) {
     return kCols + kDeltaChunk * (2 * ns + 1) * 16;
   }
@@ -305,15 +308,12 @@ struct WalkShape {
 };
 
 // One (sequence, head) and `ns` = blockDim.x / 128 slices of its dv rows, a team
-// of four warps each, and a warp that loads.  NO: parts of the operands in the
-// output's products, two (16 bits) where it is rounded to bf16, three (24) where it is
-// fp32; 0: the gradient's forward pass, which writes no output and keeps the states at
-// the chunks' starts and E.
-template <int DK, int NO>
+// of four warps each, and a warp that loads.  SAVE: the gradient's forward pass, which
+// writes no output and keeps the states at the chunks' starts and E.
+template <int DK, bool SAVE>
 __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  using W = WalkShape<DK, NO>;
-  constexpr bool SAVE = NO == 0;
+  using W = WalkShape<DK, SAVE>;
   const int ns = blockDim.x / kTeam, tid = threadIdx.x, lane = tid & 31, slice = tid / kTeam;
   // the teams take their tokens in opposite orders: the triangle's long rows of
   // one share a scheduler with the short rows of the other
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
     const float* gate = reinterpret_cast<const float*>(st + W::kGate) + 16 * w + t2;  // this warp's tokens
     const int64_t ch = (chunk0 + c) * a.Hv + h;
     float X[2][4], O[2][4];
-    state_times_rows<DK, NO>(own, sk, sk + W::kTile, w, lane, X, O);
+    state_times_rows<DK, SAVE ? 0 : 3>(own, sk, sk + W::kTile, w, lane, X, O);
     {
       // X = V - e^G (K S^T), O = scale e^G (Q S^T)
       uint32_t v[4];
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
         }
       }
       put_tiles<3>(own + W::kW, w, V[0], V[1], lane);
-      if constexpr (!SAVE) put_tiles<NO>(own + W::kU, w, U[0], U[1], lane);
+      if constexpr (!SAVE) put_tiles<3>(own + W::kU, w, U[0], U[1], lane);
     }
     {
       uint32_t bk[4][DK / 64][4];
@@ -437,14 +437,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
     }
     if constexpr (!SAVE) {
       // O += M U, this warp's tokens
-      uint32_t bm[4][NO][4];
-      float T[2][4];
-      load_map<false, NO>(bm, se + 3 * kImage, w, lane);
-      map_tokens<false, NO>(own + W::kU, bm, w, lane, T);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) O[i][e] += T[i][e];
+      add_map_tokens(own + W::kU, se + 3 * kImage, w, lane, O);
     }
     const int n = min(kDeltaChunk, len - c * kDeltaChunk) - 16 * w;  // this warp's tokens, if any
     const int64_t orow = b * a.T + tok0 + int64_t(c) * kDeltaChunk + 16 * w;
@@ -472,14 +465,14 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
   if (a.state_out) store_state<DK>(S, a.state_out, srow, w, lane);
 }
 
-template <int DK, int NO>
+template <int DK, bool SAVE>
 cudaError_t run_walk(const LaunchEnv& env, const WalkArgs& w) {
-  using W = WalkShape<DK, NO>;
+  using W = WalkShape<DK, SAVE>;
   const int ns = walk_slices(w.map.ndocs, w.Hv, w.dv, env.num_sms);
-  const cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<DK, NO>,
+  const cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<DK, SAVE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, W::smem(2));
   if (e != cudaSuccess) return e;
-  return launch_pdl(delta_walk_kernel<DK, NO>,
+  return launch_pdl(delta_walk_kernel<DK, SAVE>,
                     dim3(unsigned(w.map.ndocs * w.Hv * (w.dv / (16 * ns)))),
                     dim3(kTeam * ns + 32),
                     W::smem(ns), env.stream, w);
@@ -678,10 +671,9 @@ cudaError_t launch_team_walk(const LaunchEnv& env, const DeltaArgs& a, const uns
   w.status = env.status;
   if (save) {
     w.save = *save;
-    return a.dk == 64 ? run_walk<64, 0>(env, w) : run_walk<128, 0>(env, w);
+    return a.dk == 64 ? run_walk<64, true>(env, w) : run_walk<128, true>(env, w);
   }
-  if (a.out_fp32) return a.dk == 64 ? run_walk<64, 3>(env, w) : run_walk<128, 3>(env, w);
-  return a.dk == 64 ? run_walk<64, 2>(env, w) : run_walk<128, 2>(env, w);
+  return a.dk == 64 ? run_walk<64, false>(env, w) : run_walk<128, false>(env, w);
 }
 
 cudaError_t launch_delta_chunked(const LaunchEnv& env, const DeltaArgs& a) {

@@ -8,13 +8,12 @@
 // bounds it is their sum: 24 to 48 products of 64 columns (800 to 1600 cycles) and
 // then 1000 to 2000 cycles in which the 16 warps read, scale, split and write, at
 // 0.4 to 0.5 instructions a cycle and scheduler.  24001 tokens in 7 documents, 16
-// heads of 64 x 128: 261 us, as long as its longest document, 8100 cycles a chunk;
-// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 277 and 375 us,
+// heads of 64 x 128: 277 us, as long as its longest document, 8600 cycles a chunk;
+// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 276 and 375 us,
 // 8400 and 11300 cycles a chunk (with the snapshots stored ahead of the products some
 // 40 us more; with shared memory read through generic addresses, whose registers then
 // spill, 20 to 40 more).
 #include <algorithm>
-#include <type_traits>
 
 #include "delta.cuh"
 
@@ -112,7 +111,7 @@ struct TcArgs {
   bool out_fp32;
   const unsigned char* blocks;
   unsigned int* status;
-  DeltaSave save;  // NO = 0 only
+  DeltaSave save;  // kSaved only
 };
 
 constexpr int kTcWarps = 16;  // compute warps: four threads a row of the state
@@ -174,24 +173,24 @@ constexpr uint32_t kTmS = 0, kTmW = 0, kTmU = 96, kTmX = 192, kTmO = 192, kTmP =
 // Shared memory: two stages of what the products read (K, E map, for the output Q and
 // the scores) and of V and the gates, then what leaves: the output in bf16, or E in
 // three parts.
-template <int DK, int NO>
+enum HeadOut { kOutBf16, kOutFp32, kSaved };  // what leaves; kSaved: the gradient's forward pass
+template <int DK, HeadOut OUT>
 struct TcShape {
   static constexpr uint32_t kTile = kDeltaChunk * DK * 2;
-  static constexpr uint32_t kQ = kTile, kE = (NO ? 2 : 1) * kTile, kM = kE + 3 * kWideTile;
-  static constexpr uint32_t kTiles = kM + NO * kWideTile;  // what the products read
+  static constexpr uint32_t kQ = kTile, kE = (OUT == kSaved ? 1 : 2) * kTile, kM = kE + 3 * kWideTile;
+  static constexpr uint32_t kTiles = kM + (OUT == kSaved ? 0 : 3 * kWideTile);  // what the products read
   static constexpr uint32_t kV = 0, kGate = kDeltaChunk * 256, kRest = kGate + 768;
   static constexpr uint32_t kOut = 2 * kTiles + 2 * kRest;
-  static constexpr uint32_t kBars = kOut + (NO == 0 ? 3 * kTokTile : NO == 2 ? kDeltaChunk * 256 : 0);
-  static constexpr int64_t kBlock = NO ? kWideFwd : kWideGrad;
+  static constexpr uint32_t kBars = kOut + (OUT == kSaved ? 3 * kTokTile : OUT == kOutBf16 ? kDeltaChunk * 256 : 0);
+  static constexpr int64_t kBlock = OUT == kSaved ? kWideGrad : kWideFwd;
   static constexpr uint32_t kSmem = kBars + sizeof(TcBars) + 1024;
 };
 
-// NO: as in delta_walk_kernel.
-template <int DK, int NO>
+template <int DK, HeadOut OUT>
 __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  using W = TcShape<DK, NO>;
-  constexpr bool SAVE = NO == 0;
+  using W = TcShape<DK, OUT>;
+  constexpr bool SAVE = OUT == kSaved;
   constexpr int HS = DK / 4;  // columns of the state a thread
   constexpr uint32_t SP = DK / 2;  // columns of tensor memory a part of the state
   unsigned char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // an offset: its loads stay shared ones
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         __syncwarp();
       }
       bulk_wait_group_all();
-    } else if (lw == 2 && NO == 2) {
+    } else if (lw == 2 && OUT == kOutBf16) {
       auto* out = static_cast<__nv_bfloat16*>(a.out) + ((b * a.T + tok0) * a.Hv + h) * a.dv + row0;
       const int64_t step = int64_t(a.Hv) * a.dv;
       for (int c = 0; c < nchunks; ++c, out += kDeltaChunk * step) {
@@ -273,8 +272,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
         if (lw == 0 && lane == 0) {
           const unsigned char* blk = a.blocks + ((chunk0 + c) * a.Hv + h) * W::kBlock;
-          mbar_arrive_expect_tx(&bars->full[st], (3 + NO) * kWideTile + 768);
-          bulk_load(tiles + W::kE, blk, (3 + NO) * kWideTile, &bars->full[st]);
+          mbar_arrive_expect_tx(&bars->full[st], (SAVE ? 3 : 6) * kWideTile + 768);
+          bulk_load(tiles + W::kE, blk, (SAVE ? 3 : 6) * kWideTile, &bars->full[st]);
           bulk_load(rest + W::kGate, blk + kWideGate, 768, &bars->full[st]);
         }
         __syncwarp();
@@ -301,19 +300,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       const int st = c & 1;
       const uint32_t par = c & 1, sk = base + st * (W::kTiles >> 4);
       asm volatile("" : "+r"(tmu));  // operand addresses are not kept, as by again()
-      // a triangular map's product with the NP parts at `x`, small terms first;
+      // a triangular map's product with the parts at `x`, small terms first;
       // tokens before a step's do not see it
-      auto map = [&](uint32_t d, uint32_t x, uint32_t tile, auto np) {
-        constexpr int NP = decltype(np)::value;
+      auto map = [&](uint32_t d, uint32_t x, uint32_t tile) {
 #pragma unroll
-        for (int sum = NP - 1; sum >= 0; --sum)
+        for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
           for (int p = 0; p <= sum; ++p)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               mma_ts(on, d + 16 * ks, x + p * 32 + ks * 8,
                      tile + (((sum - p) * kWideTile + ks * (16 * 128 + 32)) >> 4),
-                     idesc_bf16_f32(128, 64 - 16 * ks, false, false), sum < NP - 1 || p > 0 || ks > 0);
+                     idesc_bf16_f32(128, 64 - 16 * ks, false, false), sum < 2 || p > 0 || ks > 0);
       };
       wait(&bars->full[st], (c >> 1) & 1);
       wait(&bars->s_ready, par);
@@ -327,16 +325,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       commit(on, &bars->p_done);
       if constexpr (!SAVE) {
 #pragma unroll
-        for (int p = NO - 1; p >= 0; --p)
+        for (int p = 2; p >= 0; --p)
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
             mma_ts(on, tmu + kTmD, tmu + kTmS + p * SP + ks * 8,
-                   sk + ((W::kQ + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_tok, p < NO - 1 || ks > 0);
+                   sk + ((W::kQ + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_tok, p < 2 || ks > 0);
         commit(on, &bars->q_done);
       }
       wait(&bars->x_ready, par);
       tc_fence_after_sync();
-      map(tmu + kTmP, tmu + kTmX, sk + (W::kE >> 4), std::integral_constant<int, 3>());
+      map(tmu + kTmP, tmu + kTmX, sk + (W::kE >> 4));
       commit(on, &bars->e_done);
       wait(&bars->w_ready, par);
       tc_fence_after_sync();
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       if constexpr (!SAVE) {
         wait(&bars->u_ready, par);
         tc_fence_after_sync();
-        map(tmu + kTmO, tmu + kTmU, sk + (W::kM >> 4), std::integral_constant<int, NO>());
+        map(tmu + kTmO, tmu + kTmU, sk + (W::kM >> 4));
         commit(on, &bars->m_done);
       }
       commit(on, &bars->empty[st]);
@@ -401,14 +399,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       }
     };
     auto finish_out = [&](int c) {
-      if constexpr (NO == 2) {
+      if constexpr (OUT == kOutBf16) {
         if (c > 0) wait(&bars->out_free, (c - 1) & 1);
         unsigned char* to = smem + W::kOut + kTok * quarter * 256 + row * 2;
 #pragma unroll
         for (int e = 0; e < kTok; ++e) *reinterpret_cast<__nv_bfloat16*>(to + e * 256) = __float2bfloat16_rn(O[e]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->out_ready[c & 1]);
-      } else if constexpr (NO == 3) {
+      } else if constexpr (OUT == kOutFp32) {
         const int n = min(kDeltaChunk, len - c * kDeltaChunk) - kTok * quarter;
         float* out = static_cast<float*>(a.out) +
                      ((b * a.T + tok0 + int64_t(c) * kDeltaChunk + kTok * quarter) * a.Hv + h) * a.dv + row0 + row;
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
           x[e + 2] *= be.z;
           x[e + 3] *= be.w;
         }
-        put16<NO>(trow + kTmU + kTok / 2 * quarter, 32, x);
+        put16<3>(trow + kTmU + kTok / 2 * quarter, 32, x);
         arrive(&bars->u_ready);
         if (lane == 0) mbar_arrive(&bars->empty[st]);  // V and the gates are read
       }
@@ -847,9 +845,9 @@ cudaError_t run_head(const LaunchEnv& env, K kernel, uint32_t smem, const A& a) 
   return launch_pdl(kernel, dim3(unsigned(a.map.ndocs * a.Hv * ((a.dv + 127) / 128))), dim3(kTcThreads), smem,
                     env.stream, a);
 }
-template <int DK, int NO>
+template <int DK, HeadOut OUT>
 cudaError_t run_head_walk(const LaunchEnv& env, const TcArgs& a) {
-  return run_head(env, head_walk_kernel<DK, NO>, TcShape<DK, NO>::kSmem, a);
+  return run_head(env, head_walk_kernel<DK, OUT>, TcShape<DK, OUT>::kSmem, a);
 }
 
 }  // namespace
@@ -874,10 +872,10 @@ cudaError_t launch_head_walk(const LaunchEnv& env, const DeltaArgs& f, const uns
   a.status = env.status;
   if (save) {
     a.save = *save;
-    return f.dk == 64 ? run_head_walk<64, 0>(env, a) : run_head_walk<128, 0>(env, a);
+    return f.dk == 64 ? run_head_walk<64, kSaved>(env, a) : run_head_walk<128, kSaved>(env, a);
   }
-  if (f.out_fp32) return f.dk == 64 ? run_head_walk<64, 3>(env, a) : run_head_walk<128, 3>(env, a);
-  return f.dk == 64 ? run_head_walk<64, 2>(env, a) : run_head_walk<128, 2>(env, a);
+  if (f.out_fp32) return f.dk == 64 ? run_head_walk<64, kOutFp32>(env, a) : run_head_walk<128, kOutFp32>(env, a);
+  return f.dk == 64 ? run_head_walk<64, kOutBf16>(env, a) : run_head_walk<128, kOutBf16>(env, a);
 }
 
 cudaError_t launch_head_reverse(const LaunchEnv& env, const ReverseArgs& r, int dk) {

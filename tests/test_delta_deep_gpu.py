@@ -146,3 +146,20 @@ def test_gate_gradient_of_every_token(cuda_device, B, dk, dv):
     size = got[3].double().abs().sum((0, 1))
     # the difference's own error: h^2 / 6 of the third derivative, and 1e-16 of the loss / h
     assert torch.all((slope - mine).abs() <= 2.0 ** -12 * size + 1e-8), (slope, mine)
+
+
+def wrongly_rounded(got, ref):
+    return float((got != ref.to(torch.bfloat16)).double().mean())
+
+
+@pytest.mark.parametrize("B,dk,dv", [(1, 128, 64), (2, 64, 128), (20, 128, 96), (20, 64, 128)])
+def test_bf16_results_are_rounded_once(cuda_device, B, dk, dv):
+    """Every product has operands of 24 bits, so a bf16 result is the exact value's
+    rounding but where that lies between two bf16 numbers by no more than the error.
+    An error of 2^-21 of a head's typical value (24 bits, some sums) moves about
+    2 * 2^-21 / 2^-8 of the elements of that size, and some eight times as many with
+    the small ones: 2^-9 * 2^-2 = 2^-11.  (Operands of 16 bits move 32 times as many.)"""
+    T, Hv = 300, 4
+    assert by_head(B, Hv, dv) == (B == 20)
+    x, S0, dS1, do = inputs(B, B, T, 2, Hv, dk, dv)
+    assert wrongly_rounded(seq.call(x, state_in=S0), seq.reference(x, dk ** -0.5, S0)[0]) <= 2.0 ** -11
