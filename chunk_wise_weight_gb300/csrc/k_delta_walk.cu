@@ -9,8 +9,8 @@
 // then 1000 to 2000 cycles in which the 16 warps read, scale, split and write, at
 // 0.4 to 0.5 instructions a cycle and scheduler.  24001 tokens in 7 documents, 16
 // heads of 64 x 128: 277 us, as long as its longest document, 8600 cycles a chunk;
-// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 276 and 375 us,
-// 8400 and 11300 cycles a chunk (with the snapshots stored ahead of the products some
+// the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 276 and 338 us,
+// 8400 and 10200 cycles a chunk (with the snapshots stored ahead of the products some
 // 40 us more; with shared memory read through generic addresses, whose registers then
 // spill, 20 to 40 more).
 #include <algorithm>
@@ -548,6 +548,11 @@ struct BackShape {
 // Tensor memory as in the forward walk; the parts of scale e^G dO take U's place,
 // M^T dO that of Q S^T.
 constexpr uint32_t kTmY = 96;
+// (e^G dX)^T K has an accumulator of its own, over X's parts and dR, which are read by
+// then: added to the other product's full-size sum, each step's rounding towards zero
+// is one more of the sum's last place (the starting states' gradient was off by 4.8e-7
+// in the Frobenius norm, 1.5e-7 now), and the two need not wait for one another (375 us, 338 now).
+constexpr uint32_t kTmE = 192;
 
 // The reverse walk of a head, with dS in the state's place.
 template <int DK>
@@ -708,7 +713,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       for (int p = 2; p >= 0; --p)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_ts(on, tmu + kTmD, tmu + kTmW + p * 32 + ks * 8, sk + lbo + ((ks * 2048) >> 4), id_state, 1);
+          mma_ts(on, tmu + kTmE, tmu + kTmW + p * 32 + ks * 8, sk + lbo + ((ks * 2048) >> 4), id_state, p < 2 || ks > 0);
       commit(on, &bars->d_done);
       commit(on, &bars->empty[st]);
     }
@@ -821,10 +826,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
       tc_fence_after_sync();
 #pragma unroll
       for (int i = 0; i < HS; i += 16) {
-        float v[16];
+        float v[16], x2[16];
         read16(trow + kTmD + quarter * HS + i, v);
+        read16(trow + kTmE + quarter * HS + i, x2);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[i + e] = last * S[i + e] + v[e];
+        for (int e = 0; e < 16; ++e) S[i + e] = last * S[i + e] + (v[e] + x2[e]);
       }
     }
     if (active && a.dstate_in)
