@@ -21,9 +21,9 @@
 //
 // Four kernels: the chunks' blocks and the forward walk (k_delta.cu) keep S and E; a
 // reverse walk, of the same shape, carries dS and leaves dR and dS'; then everything
-// else, of every chunk at once.  2 x 4096 tokens, 20 heads of 128 x 128: 95 + 277 + 375 +
-// 379 us; bound by the two walks' chains and by the last kernel's passes, which follow one
-// another.
+// else, of every chunk at once.  2 x 4096 tokens, 20 heads of 128 x 128: 95 + 276 + 338 +
+// 345 us; bound by the two walks' chains and by the last kernel's passes, whose products
+// and sums take turns.
 #include <algorithm>
 
 #include "delta.cuh"
@@ -243,40 +243,42 @@ constexpr int kKeyThreads = 512;
 // of 128-byte rows, swizzled:
 //   dO      [64 tokens, then 64 rows of zeros][dv]
 //   dR, E   [3 parts][rows of dv][64 tokens]
-//   states  [3 parts][pieces of 8 dk][rows of dv], not swizzled: S, then dS'
+//   S, dS'  [3 parts][pieces of 8 dk][rows of dv], not swizzled
 //   Q, K    [blocks of 64 dk][64 tokens of Q, then of K]
-//   P       [3 parts][P1, L][64 rows][64 columns]
+//   P       [3 parts][P1, L][64 rows][64 columns], over dR, which is used up by then
 // and what dg is summed from.
 struct KeyShape {
   static constexpr uint32_t kSeg = 8192;
   static constexpr uint32_t kZero = kSeg;  // the zeros below dO
-  static constexpr uint32_t kX = 2 * kSeg, kTokPart = kSeg, kE = kX + 3 * kTokPart;
-  static constexpr uint32_t kState = kE + 3 * kTokPart, kStatePart = 2 * kSeg;
-  static constexpr uint32_t kQ = kState + 3 * kStatePart, kBlock = 2 * kSeg, kK = kQ + kSeg;
-  static constexpr uint32_t kP = kQ + 2 * kBlock, kPPart = 2 * kSeg;
-  static constexpr uint32_t kSums = kP + 3 * kPPart;
+  static constexpr uint32_t kX = 2 * kSeg, kTokPart = kSeg;
+  static constexpr uint32_t kP = kX, kPPart = 2 * kSeg;
+  static constexpr uint32_t kE = kP + 3 * kPPart;
+  static constexpr uint32_t kState = kE + 3 * kTokPart, kStatePart = 2 * kSeg, kState1 = kState + 3 * kStatePart;
+  static constexpr uint32_t kQ = kState1 + 3 * kStatePart, kBlock = 2 * kSeg, kK = kQ + kSeg;
+  static constexpr uint32_t kSums = kQ + 2 * kBlock;
 };
 struct KeySums {
-  Pair G[kDeltaChunk];
-  float gate[3][kDeltaChunk];  // e^G, e^{G_63 - G}, beta
-  float a[4][128];             // by quarter of dk: a_i, its part of dq and that of dk
+  Pair G[2][kDeltaChunk];         // of this head and the next
+  float gate[2][3][kDeltaChunk];  // e^G, e^{G_63 - G}, beta
+  float a[4][128];                // by quarter of dk: a_i, its part of dq and that of dk
   float c[4][kDeltaChunk];
-  float b[4][128];             // sums of B_ij over a quarter of the columns
-  float r[4][kDeltaChunk];     // by 32 rows i: sum of B_ij over i >= t > j
-  float d[kKeyThreads / 32];   // <dS', S>
+  float b[4][128];                // sums of B_ij over a quarter of the columns
+  float r[4][kDeltaChunk];        // by 32 rows i: sum of B_ij over i >= t > j
+  float d[kKeyThreads / 32];      // <dS', S>
 };
 struct KeyBars {
-  uint64_t loaded, loaded_d, done_s, done;
+  uint64_t s, r, e, d;  // S, dR, E, dS' are loaded
+  uint64_t done_s, done_d, done_p;
   uint32_t tmem;
   int abort;
 };
-// Columns of tensor memory: [dO; dR] E^T, [dO; dR] S, [0; E] dS', the sums of P's
-// products over the value heads, [Q; K] K^T.
+// Columns of tensor memory: [dO; dR] E^T; [dO; dR] S, then P1^T Q + L^T K; [0; E] dS';
+// [P1; L] K; [Q; K] K^T.
 constexpr uint32_t kTmP = 0, kTmS = 64, kTmD = 192, kTmK = 320, kTmQ = 448;
 
 // dg of a chunk and head, by one warp, two tokens a lane.  Sums run from the far end
 // (nothing is subtracted), so small ones keep their digits.
-__device__ __forceinline__ void gate_gradient(const KeySums& s, float* dg, int64_t stride, int n, int lane) {
+__device__ __forceinline__ void gate_gradient(const KeySums& s, int set, float* dg, int64_t stride, int n, int lane) {
   const int t0 = 2 * lane;
   float a[2], c[2], r[2], d = lane < kKeyThreads / 32 ? s.d[lane] : 0.f;
 #pragma unroll
@@ -291,7 +293,7 @@ __device__ __forceinline__ void gate_gradient(const KeySums& s, float* dg, int64
   }
 #pragma unroll
   for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(~0u, d, m);
-  d *= s.gate[0][63];
+  d *= s.gate[set][0][63];
   float after = a[0] + a[1], before = c[0] + c[1];
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -309,17 +311,22 @@ __device__ __forceinline__ void gate_gradient(const KeySums& s, float* dg, int64
 
 // One (chunk, key head), on the tensor cores: 128 accumulator rows, dq's 64
 // tokens above dk's 64.  Once: [Q; K] K^T.  For each value head that shares the key
-// head, in order, with U = b E and dX = b dR:
-//   [dO; dR] E^T -> with the decays and betas P1 (rows of dq) and L (below the
-//     diagonal); its lower diagonal is dbeta; with [Q; K] K^T the B_ij of dg
+// head, in order, with U = b E and dX = b dR, by panels of dv:
+//   [dO; dR] E^T, added over the panels in registers -> with the decays and betas P1
+//     (rows of dq) and L (below the diagonal); its lower diagonal is dbeta; with
+//     [Q; K] K^T the B_ij of dg
 //   [dO; dR] S, [0; E] dS': scaled by row and added in registers; dotted with q and k
 //     the a_i and c_j of dg
-//   [P1; L] K + [0; P1^T] Q + [0; L^T] K: added over the heads in tensor memory
+// and then [P1; L] K and [0; P1^T] Q + [0; L^T] K, added in registers.
 // A transposed left operand is a second group of 64 rows below one of zeros.
 // Operands that are not bf16 as given have three parts, and products of parts p, r
-// are kept for p + r < 3, as in the walks.  128 chunks of 10 key heads, two value heads of
-// 128 x 128 each: 379 us, of which 112 would be the bytes (755 MB, mostly states) and 110
-// the products; a pass's loads, products and sums follow one another.
+// are kept for p + r < 3, as in the walks.  Sums over panels and heads are in
+// registers because each addition in tensor memory rounds the full-size sum towards
+// zero (in tensor memory dbeta's error in the Frobenius norm was 7.7e-7, now 3.1e-7).
+// What a pass has used up is loaded anew at once, so that the next one's operands
+// arrive under its remaining products and sums.  128 chunks of 10 key heads, two value
+// heads of 128 x 128 each: 345 us, of which 112 would be the bytes (755 MB, mostly
+// states) and 130 the products; products and the sums that wait for them take turns.
 template <int DK>
 __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradArgs a) {
   extern __shared__ unsigned char smem_raw[];
@@ -335,10 +342,8 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   const int tok = row & 63;
   const bool is_k = row >= 64;
   if (tid == 0) {
-    mbar_init(&bars->loaded, 1);
-    mbar_init(&bars->loaded_d, 1);
-    mbar_init(&bars->done_s, 1);
-    mbar_init(&bars->done, 1);
+    for (uint64_t* bar : {&bars->s, &bars->r, &bars->e, &bars->d, &bars->done_s, &bars->done_d, &bars->done_p})
+      mbar_init(bar, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   const uint32_t trow = tm + (uint32_t((warp & 3) * 32) << 16);
   griddep_wait();
   griddep_launch_dependents();
-  const int chunk = blockIdx.x, hk = blockIdx.y, group = a.Hv / a.Hk;
+  const int chunk = blockIdx.x, hk = blockIdx.y, group = a.Hv / a.Hk, h_end = (hk + 1) * group;
   const int s = a.map.doc_of(chunk);
   const int t0 = (chunk - a.map.chunk0(s)) * kDeltaChunk;
   const int n = min(kDeltaChunk, a.map.len(s) - t0);
@@ -361,6 +366,55 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!mbar_wait(bar, parity, &bars->abort)) raise_abort(&bars->abort, a.status, kStatusTimeout);
   };
+  // Loads of a panel's operands, by one thread: three parts each.
+  auto head = [&](int h) { return int64_t(chunk) * a.Hv + h; };
+  auto load_states = [&](const unsigned char* from, int h, int v0, uint32_t to, uint64_t* bar) {
+    const uint32_t bytes = uint32_t(min(kPanel, a.dv - v0)) * DK * 2;
+    from += head(h) * state_parts(a.dv, DK) + state_parts(v0, DK);
+    mbar_arrive_expect_tx(bar, 3 * bytes);
+    for (int p = 0; p < 3; ++p) bulk_load(smem + to + p * W::kStatePart, from + p * bytes, bytes, bar);
+  };
+  auto load_tokens = [&](const unsigned char* from, int h, int v0, uint32_t to, uint64_t* bar) {
+    const uint32_t bytes = uint32_t(min(kPanel, a.dv - v0)) * 128;
+    from += head(h) * token_tiles(a.dv) + int64_t(v0) * 128;
+    mbar_arrive_expect_tx(bar, 3 * bytes);
+    for (int p = 0; p < 3; ++p) bulk_load(smem + to + p * W::kTokPart, from + int64_t(p) * a.dv * 128, bytes, bar);
+  };
+  // dO of a panel: one piece of 8 a thread
+  static_assert(kKeyThreads == kDeltaChunk * 8, "a piece of dO, and of the zeros, a thread");
+  auto load_do = [&](int h, int v0) {
+    const int r = tid >> 3, p = tid & 7;
+    if (p * 8 < min(kPanel, a.dv - v0)) {
+      unsigned char* d = smem + tile_at<8>(r, p);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.dout.data) + b * a.dout.sb + t * a.dout.st +
+                                 h * a.dout.sh + v0 + p * 8 + (r < n ? r * a.dout.st : 0);
+      if (a.dout.vec)
+        cp16(smem_u32(d), src, r < n);
+      else if (r < n)
+        store_piece(d, src);
+      else
+        *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+    }
+    cp_commit();
+  };
+  // a head's gates and their sums, by two warps
+  auto load_gates = [&](int h) {
+    const int set = h & 1;
+    if (warp == 1) {
+      const float* from = reinterpret_cast<const float*>(a.blocks + head(h) * a.block_bytes + a.gate_at);
+#pragma unroll
+      for (int i = 0; i < 3 * kDeltaChunk; i += 32) (&sums.gate[set][0][0])[i + lane] = from[i + lane];
+    } else if (warp == 2) {
+      gate_sums(a.g, b, t, h, n, lane, sums.G[set]);
+    }
+  };
+  if (tid == 0) {
+    load_tokens(a.dr, hk * group, 0, W::kX, &bars->r);
+    load_tokens(a.e, hk * group, 0, W::kE, &bars->e);
+    load_states(a.snap, hk * group, 0, W::kState, &bars->s);
+    load_states(a.dsnap, hk * group, 0, W::kState1, &bars->d);
+  }
+  __syncwarp();
   {
     const auto* kp = static_cast<const __nv_bfloat16*>(a.k.data) + b * a.k.sb + t * a.k.st + hk * a.k.sh;
     const auto* qp = static_cast<const __nv_bfloat16*>(a.q.data) + b * a.q.sb + t * a.q.st + hk * a.q.sh;
@@ -369,22 +423,22 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
       load_tile<8>(smem + W::kQ + i * W::kBlock, qp + 64 * i, a.q.st, n, a.q.vec, tid, kKeyThreads);
       load_tile<8>(smem + W::kK + i * W::kBlock, kp + 64 * i, a.k.st, n, a.k.vec, tid, kKeyThreads);
     }
-    static_assert(kKeyThreads * 16 == W::kSeg, "one piece of the zeros a thread");
     *reinterpret_cast<uint4*>(smem + W::kZero + tid * 16) = make_uint4(0, 0, 0, 0);
   }
+  load_do(hk * group, 0);
+  load_gates(hk * group);
   // left operand by rows or transposed; right operands have their rows along the
   // sum, but for K in [Q; K] K^T
   constexpr uint32_t id_p = idesc_bf16_f32(128, 64, false, true), id_pt = idesc_bf16_f32(128, 64, true, true);
   constexpr uint32_t id_s = idesc_bf16_f32(128, DK, false, true), id_st = idesc_bf16_f32(128, DK, true, true);
   constexpr uint32_t id_q = idesc_bf16_f32(128, 64, false, false);
   // low words of descriptors: an operand; one below 64 rows of zeros
-  const uint32_t su = __shfl_sync(~0u, sb, 0), tmu = __shfl_sync(~0u, tm, 0);
-  const uint32_t zeros = (su + W::kZero) >> 4;
-  auto lo = [&](uint32_t at, uint32_t lbo = 16) { return ((su + at) >> 4) | (lbo >> 4) << 16; };
-  auto below = [&](uint32_t at) { return zeros | (((su + at) >> 4) - zeros) << 16; };
+  uint32_t base = __shfl_sync(~0u, sb, 0) >> 4;
+  const uint32_t tmu = __shfl_sync(~0u, tm, 0);
+  auto lo = [&](uint32_t at, uint32_t lbo = 16) { return base + ((at >> 4) | (lbo >> 4) << 16); };
+  auto below = [&](uint32_t at) { return base + ((W::kZero >> 4) | ((at - W::kZero) >> 4) << 16); };
   // A head's operands, most of what is read, come as far as L2 while the products
-  // of the one before run, this CTA's or the last one's on this SM: the loads of a
-  // pass fill shared memory, so that nothing else overlaps them.
+  // of the one before run, this CTA's or the last one's on this SM.
   auto fetch = [&](int64_t linear, int h_next) {
     const int64_t at = (linear % gridDim.x) * a.Hv + h_next;
     prefetch_bulk(a.snap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
@@ -393,7 +447,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
     prefetch_bulk(a.dsnap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
   };
   const int64_t here = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, after = here + a.ahead;
-  float acc[HC];
+  float acc[HC], P[16];
 #pragma unroll
   for (int e = 0; e < HC; ++e) acc[e] = 0.f;
   // this thread's row of [Q; K], 8 columns from `piece` of its quarter, dotted with v
@@ -410,134 +464,140 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
     return sum;
   };
   uint32_t it = 0;  // passes over a panel
-  for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    const int64_t ch = int64_t(chunk) * a.Hv + h;
-    const auto* dop = static_cast<const __nv_bfloat16*>(a.dout.data) + b * a.dout.sb + t * a.dout.st + h * a.dout.sh;
-    float dot = 0.f;  // <dS', S>
+  for (int h = hk * group; h < h_end; ++h) {
+    const int set = h & 1;
+    float dot = 0.f, part_a = 0.f, part_c = 0.f;  // <dS', S>; this row's a_i and c_j
+#pragma unroll
+    for (int i = 0; i < 16; ++i) P[i] = 0.f;
     for (int v0 = 0; v0 < a.dv; v0 += kPanel, ++it) {
-      const int width = min(kPanel, a.dv - v0);
+      const int width = min(kPanel, a.dv - v0), steps = width / 16;
       const uint32_t par = it & 1;
       const bool last = v0 + kPanel >= a.dv;
-      const uint32_t state_bytes = uint32_t(width) * DK * 2;  // one part
+      const int next_h = last ? h + 1 : h, next_v = last ? 0 : v0 + kPanel;
+      const bool more = next_h < h_end;
       // the states' descriptor: core matrices of 8 rows of dv by 16 bytes of dk,
       // 128 bytes apart along the rows, width * 16 along dk
       const uint32_t state_hi = uint32_t(width) | (1u << 14);
-      auto state = [&](int p, int ks) { return lo(W::kState + p * W::kStatePart + ks * 256, 128); };
-      if (tid == 0) {
-        const int64_t tiles = ch * token_tiles(a.dv) + int64_t(v0) * 128;
-        const unsigned char* ss = a.snap + ch * state_parts(a.dv, DK) + state_parts(v0, DK);
-        mbar_arrive_expect_tx(&bars->loaded, uint32_t(6 * width * 128) + 3 * state_bytes);
-        for (int p = 0; p < 3; ++p) {
-          bulk_load(smem + W::kX + p * W::kTokPart, a.dr + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
-          bulk_load(smem + W::kE + p * W::kTokPart, a.e + tiles + int64_t(p) * a.dv * 128, uint32_t(width * 128), &bars->loaded);
-        }
-        for (int p = 0; p < 3; ++p)
-          bulk_load(smem + W::kState + p * W::kStatePart, ss + p * state_bytes, state_bytes, &bars->loaded);
-      }
-      {
-        static_assert(kKeyThreads == kDeltaChunk * 8, "one piece of dO a thread");
-        const int r = tid >> 3, p = tid & 7;
-        if (p * 8 < width) {
-          unsigned char* d = smem + tile_at<8>(r, p);
-          const __nv_bfloat16* src = dop + v0 + p * 8 + (r < n ? r * a.dout.st : 0);
-          if (a.dout.vec)
-            cp16(smem_u32(d), src, r < n);
-          else if (r < n)
-            store_piece(d, src);
-          else
-            *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
-        }
-      }
-      cp_commit();
       cp_wait<0>();
       fence_proxy_async_smem();
       tc_fence_before_sync();
-      __syncthreads();
+      __syncthreads();  // dO; the accumulators are read, last pass's sums too
       if (warp == 0) {
         const uint32_t on = elect_one();
+        asm volatile("" : "+r"(base));  // descriptors are worked out anew, not kept in registers
         tc_fence_after_sync();
         if (it == 0)
 #pragma unroll
           for (int ks = 0; ks < DK / 16; ++ks)
             mma_ss(on, tmu + kTmQ, lo(W::kQ + (ks >> 2) * W::kBlock + (ks & 3) * 32),
                    lo(W::kK + (ks >> 2) * W::kBlock + (ks & 3) * 32), id_q, ks > 0);
-        wait(&bars->loaded, par);
+        wait(&bars->r, par);
+        wait(&bars->e, par);
+        wait(&bars->s, par);
         if (v0 == 0 && lane == 0) {
-          if (h + 1 < (hk + 1) * group)
+          if (h + 1 < h_end)
             fetch(here, h + 1);
           else if (after < int64_t(gridDim.x) * gridDim.y)
             fetch(after, int(after / gridDim.x) * group);
         }
         __syncwarp();
-        // small terms first; dO is exact, so it has no other parts
-#pragma unroll 1
-        for (int sum = 2; sum >= 0; --sum)
-#pragma unroll 1
-          for (int p = 0; p <= sum; ++p)
-#pragma unroll 2
-            for (int ks = 0; ks < width / 16; ++ks) {
-              const uint32_t dos = lo(ks * 32), be = lo(W::kE + (sum - p) * W::kTokPart + ks * 2048);
-              const uint32_t bs = state(sum - p, ks), ax = below(W::kX + p * W::kTokPart + ks * 2048);
-              if (p == 0) {
-                const bool more = v0 > 0 || sum < 2 || ks > 0;
-                mma_ss(on, tmu + kTmP, dos, be, id_p, more);
-                mma_ss(on, tmu + kTmS, dos, bs, id_s, more, state_hi);
-              }
-              mma_ss(on, tmu + kTmP, ax, be, id_pt, 1);
-              mma_ss(on, tmu + kTmS, ax, bs, id_st, 1, state_hi);
-            }
-        commit(on, &bars->done_s);
-      } else if (v0 == 0 && warp == 1) {  // meanwhile
-        const float* from = reinterpret_cast<const float*>(a.blocks + ch * a.block_bytes + a.gate_at);
+        // small terms first; dO is exact, so it has no other parts (unrolled: with
+        // descriptors worked out in loops, each product cost its issuer 100 cycles)
 #pragma unroll
-        for (int i = 0; i < 3 * kDeltaChunk; i += 32) (&sums.gate[0][0])[i + lane] = from[i + lane];
-      } else if (v0 == 0 && warp == 2) {
-        gate_sums(a.g, b, t, h, n, lane, sums.G);
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+          for (int p = 0; p <= sum; ++p)
+#pragma unroll
+            for (int ks = 0; ks < kPanel / 16; ++ks)
+              if (ks < steps) {
+                const uint32_t dos = lo(ks * 32), be = lo(W::kE + (sum - p) * W::kTokPart + ks * 2048);
+                const uint32_t bs = lo(W::kState + (sum - p) * W::kStatePart + ks * 256, 128);
+                const uint32_t ax = below(W::kX + p * W::kTokPart + ks * 2048);
+                if (p == 0) {
+                  mma_ss(on, tmu + kTmP, dos, be, id_p, sum < 2 || ks > 0);
+                  mma_ss(on, tmu + kTmS, dos, bs, id_s, sum < 2 || ks > 0, state_hi);
+                }
+                mma_ss(on, tmu + kTmP, ax, be, id_pt, 1);
+                mma_ss(on, tmu + kTmS, ax, bs, id_st, 1, state_hi);
+              }
+        commit(on, &bars->done_s);
+        wait(&bars->d, par);
+#pragma unroll
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+          for (int p = 0; p <= sum; ++p)
+#pragma unroll
+            for (int ks = 0; ks < kPanel / 16; ++ks)
+              if (ks < steps)
+                mma_ss(on, tmu + kTmD, below(W::kE + p * W::kTokPart + ks * 2048),
+                       lo(W::kState1 + (sum - p) * W::kStatePart + ks * 256, 128), id_st, sum < 2 || p > 0 || ks > 0,
+                       state_hi);
+        commit(on, &bars->done_d);
       }
       __syncwarp();
-      // this thread's share of S, which dS' will replace
-      auto share = [&](int j, float (&x)[8]) {
-        const unsigned char* at = smem + W::kState + (tid + j * kKeyThreads) * 16;
-        uint32_t w[3][4];
+      // <dS', S>, shared by the other warps
+      wait(&bars->s, par);
+      wait(&bars->d, par);
+      for (int i = warp ? tid - 32 : width * (DK / 8); i < width * (DK / 8); i += kKeyThreads - 32) {
+        float x[2][8];
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const uint4 u = *reinterpret_cast<const uint4*>(at + p * W::kStatePart);
-          w[p][0] = u.x;
-          w[p][1] = u.y;
-          w[p][2] = u.z;
-          w[p][3] = u.w;
+        for (int which = 0; which < 2; ++which) {
+          const unsigned char* at = smem + (which ? W::kState1 : W::kState) + i * 16;
+          uint32_t w[3][4];
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            const uint4 u = *reinterpret_cast<const uint4*>(at + p * W::kStatePart);
+            w[p][0] = u.x;
+            w[p][1] = u.y;
+            w[p][2] = u.z;
+            w[p][3] = u.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 hi = unpack_bf16x2(w[0][e]), mid = unpack_bf16x2(w[1][e]), low = unpack_bf16x2(w[2][e]);
+            x[which][2 * e] = hi.x + (mid.x + low.x);
+            x[which][2 * e + 1] = hi.y + (mid.y + low.y);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 hi = unpack_bf16x2(w[0][e]), mid = unpack_bf16x2(w[1][e]), low = unpack_bf16x2(w[2][e]);
-          x[2 * e] = hi.x + (mid.x + low.x);
-          x[2 * e + 1] = hi.y + (mid.y + low.y);
-        }
-      };
-      float S[NB][8];
-      wait(&bars->loaded, par);
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        if (tid + j * kKeyThreads < width * (DK / 8)) share(j, S[j]);
+        for (int e = 0; e < 8; ++e) dot += x[0][e] * x[1][e];
+      }
+      const float eg = sums.gate[set][0][tok], bt = sums.gate[set][2][tok];
       wait(&bars->done_s, par);
       tc_fence_after_sync();
-      __syncthreads();  // S is used up: dS' takes its place; the gates and their sums
-      if (tid == 0) {
-        const unsigned char* ds = a.dsnap + ch * state_parts(a.dv, DK) + state_parts(v0, DK);
-        mbar_arrive_expect_tx(&bars->loaded_d, 3 * state_bytes);
-        for (int p = 0; p < 3; ++p)
-          bulk_load(smem + W::kState + p * W::kStatePart, ds + p * state_bytes, state_bytes, &bars->loaded_d);
-      }
-      __syncwarp();
-      const float eg = sums.gate[0][tok], bt = sums.gate[2][tok];
-      float B[16];
-      if (last) {
-        // P1 and L: this thread's row, 16 columns
+      {
         float v[16];
         read16(trow + kTmP + 16 * quarter, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) P[i] += v[i];
+        const float m = is_k ? -eg * bt : a.scale * eg;
+#pragma unroll
+        for (int c0 = 0; c0 < HC; c0 += 16) {
+          read16(trow + kTmS + quarter * HC + c0, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            v[e] *= m;
+            acc[c0 + e] += v[e];
+          }
+          part_a += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
+        }
+      }
+      tc_fence_before_sync();
+      __syncthreads();  // S, dR and dO are used up
+      if (more) {
+        if (tid == 0) {
+          load_states(a.snap, next_h, next_v, W::kState, &bars->s);
+          if (!last) load_tokens(a.dr, next_h, next_v, W::kX, &bars->r);
+        }
+        __syncwarp();
+        load_do(next_h, next_v);
+        if (last) load_gates(next_h);
+      }
+      if (last) {
+        // P1 and L: this thread's row, 16 columns
+        float B[16], sum = 0.f;
         read16(trow + kTmQ + 16 * quarter, B);
-        const Pair g = sums.G[tok];
-        float sum = 0.f;
+        const Pair g = sums.G[set][tok];
 #pragma unroll
         for (int piece = 0; piece < 2; ++piece) {
           uint32_t p[4][3];
@@ -547,10 +607,10 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
               const int i = piece * 8 + 2 * e + f, c = 16 * quarter + i;
-              if (is_k && c == tok && tok < n) a.dbeta[(b * a.T + t + tok) * a.Hv + h] = v[i];  // dR.E
+              if (is_k && c == tok && tok < n) a.dbeta[(b * a.T + t + tok) * a.Hv + h] = P[i];  // dR.E
               const bool on = is_k ? c < tok : c <= tok;
-              const float d = on ? decay(g, sums.G[c]) * sums.gate[2][c] : 0.f;
-              x[f] = on ? (is_k ? -bt * d : a.scale * d) * v[i] : 0.f;
+              const float d = on ? decay(g, sums.G[set][c]) * sums.gate[set][2][c] : 0.f;
+              x[f] = on ? (is_k ? -bt * d : a.scale * d) * P[i] : 0.f;
               B[i] = c < tok ? x[f] * B[i] : 0.f;
               sum += B[i];
             }
@@ -565,35 +625,23 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
         fence_proxy_async_smem();
         tc_fence_before_sync();
         __syncthreads();
-      }
-      if (warp == 0) {
-        const uint32_t on = elect_one();
-        tc_fence_after_sync();
-        if (last) {
-#pragma unroll 1
+        if (warp == 0) {
+          const uint32_t on = elect_one();
+          asm volatile("" : "+r"(base));
+          tc_fence_after_sync();
+#pragma unroll
           for (int p = 2; p >= 0; --p)
-#pragma unroll 2
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               const uint32_t pt = W::kP + p * W::kPPart + ks * 2048;
               const uint32_t bk = lo(W::kK + ks * 2048, W::kBlock), bq = lo(W::kQ + ks * 2048, W::kBlock);
-              mma_ss(on, tmu + kTmK, lo(W::kP + p * W::kPPart + ks * 32), bk, id_s, h > hk * group || p < 2 || ks > 0);
-              mma_ss(on, tmu + kTmK, below(pt), bq, id_st, 1);
-              mma_ss(on, tmu + kTmK, below(pt + W::kSeg), bk, id_st, 1);
+              mma_ss(on, tmu + kTmK, lo(W::kP + p * W::kPPart + ks * 32), bk, id_s, p < 2 || ks > 0);
+              mma_ss(on, tmu + kTmS, below(pt), bq, id_st, p < 2 || ks > 0);
+              mma_ss(on, tmu + kTmS, below(pt + W::kSeg), bk, id_st, 1);
             }
+          commit(on, &bars->done_p);
         }
-        wait(&bars->loaded_d, par);
-#pragma unroll 1
-        for (int sum = 2; sum >= 0; --sum)
-#pragma unroll 1
-          for (int p = 0; p <= sum; ++p)
-#pragma unroll 2
-            for (int ks = 0; ks < width / 16; ++ks)
-              mma_ss(on, tmu + kTmD, below(W::kE + p * W::kTokPart + ks * 2048), state(sum - p, ks), id_st,
-                     v0 > 0 || sum < 2 || p > 0 || ks > 0, state_hi);
-        commit(on, &bars->done);
-      }
-      __syncwarp();
-      if (last) {
+        __syncwarp();
         // sum of B_ij over this warp's rows i >= t and the columns j < t
         float before = 0.f;
         for (int w = 0; w < quarter; ++w) before += sums.b[w][row];
@@ -604,77 +652,73 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
           before += x;
         }
         store_row_sums(B, sums.r[warp & 3] + 16 * quarter, lane);
-        const float m = is_k ? -eg * bt : a.scale * eg;
-        float part = 0.f;
-#pragma unroll
-        for (int c0 = 0; c0 < HC; c0 += 16) {
-          float v[16];
-          read16(trow + kTmS + quarter * HC + c0, v);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            v[e] *= m;
-            acc[c0 + e] += v[e];
-          }
-          part += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
-        }
-        sums.a[quarter][row] = part;
       }
-      wait(&bars->loaded_d, par);
-#pragma unroll
-      for (int j = 0; j < NB; ++j)
-        if (tid + j * kKeyThreads < width * (DK / 8)) {
-          float x[8];
-          share(j, x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dot += S[j][e] * x[e];
-        }
-      wait(&bars->done, par);
+      wait(&bars->done_d, par);
       tc_fence_after_sync();
-      if (last) {
-        const float m = is_k ? sums.gate[1][tok] * bt : 0.f;
-        float part = 0.f;
+      if (more && tid == 0) {
+        load_tokens(a.e, next_h, next_v, W::kE, &bars->e);
+        load_states(a.dsnap, next_h, next_v, W::kState1, &bars->d);
+      }
+      __syncwarp();
+      if (is_k) {
+        const float m = sums.gate[set][1][tok] * bt;
 #pragma unroll
         for (int c0 = 0; c0 < HC; c0 += 16) {
           float v[16];
           read16(trow + kTmD + quarter * HC + c0, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            v[e] = is_k ? m * v[e] : 0.f;
+            v[e] *= m;
             acc[c0 + e] += v[e];
           }
-          part += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
+          part_c += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);
         }
-        if (is_k) sums.c[quarter][tok] = part;
-        #pragma unroll
-        for (int m2 = 16; m2; m2 >>= 1) dot += __shfl_xor_sync(~0u, dot, m2);
-        if (lane == 0) sums.d[warp] = dot;
       }
-      tc_fence_before_sync();
-      __syncthreads();  // the panel's buffers, and the sums, are free
-      // the sums are next written behind a barrier that this warp joins later
-      if (last && warp == 3) gate_gradient(sums, a.dg + (b * a.T + t) * a.Hv + h, a.Hv, n, lane);
+      if (last) {
+        sums.a[quarter][row] = part_a;
+        if (is_k) sums.c[quarter][tok] = part_c;
+#pragma unroll
+        for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(~0u, dot, m);
+        if (lane == 0) sums.d[warp] = dot;
+        wait(&bars->done_p, (h - hk * group) & 1);
+        tc_fence_after_sync();
+        if (more && tid == 0) load_tokens(a.dr, next_h, next_v, W::kX, &bars->r);
+        __syncwarp();
+#pragma unroll
+        for (int c0 = 0; c0 < HC; c0 += 16) {
+          float v[16];
+          read16(trow + kTmK + quarter * HC + c0, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[c0 + e] += v[e];
+          if (is_k) {
+            read16(trow + kTmS + quarter * HC + c0, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[c0 + e] += v[e];
+          }
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        // its sums are next written behind a barrier that this warp joins later
+        if (warp == 3) gate_gradient(sums, set, a.dg + (b * a.T + t) * a.Hv + h, a.Hv, n, lane);
+      }
     }
   }
-  tc_fence_after_sync();
+  if (tok < n) {
+    __nv_bfloat16* to = (is_k ? a.dk : a.dq) + ((b * a.T + t + tok) * a.Hk + hk) * DK + quarter * HC;
 #pragma unroll
-  for (int c0 = 0; c0 < HC; c0 += 16) {
-    float v[16];
-    read16(trow + kTmK + quarter * HC + c0, v);
-    if (tok < n) {
-      __nv_bfloat16* to = (is_k ? a.dk : a.dq) + ((b * a.T + t + tok) * a.Hk + hk) * DK + quarter * HC + c0;
+    for (int e = 0; e < HC; e += 8) {
+      uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 16; e += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          w[f] = pack_bf16x2(acc[c0 + e + 2 * f] + v[e + 2 * f], acc[c0 + e + 2 * f + 1] + v[e + 2 * f + 1]);
-        *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int f = 0; f < 4; ++f) w[f] = pack_bf16x2(acc[e + 2 * f], acc[e + 2 * f + 1]);
+      *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tm, 512);
+  if (warp == 0) {
+    tc_fence_after_sync();
+    tmem_dealloc(tm, 512);
+  }
 }
 
 template <int DK>

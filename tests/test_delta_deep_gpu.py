@@ -163,3 +163,7 @@ def test_bf16_results_are_rounded_once(cuda_device, B, dk, dv):
     assert by_head(B, Hv, dv) == (B == 20)
     x, S0, dS1, do = inputs(B, B, T, 2, Hv, dk, dv)
     assert wrongly_rounded(seq.call(x, state_in=S0), seq.reference(x, dk ** -0.5, S0)[0]) <= 2.0 ** -11
+    got = grad.call(x, do, state_in=S0, grad_state_out=dS1)
+    ref = grad.reference(x, dk ** -0.5, S0, do, dS1)
+    for name, a, r in zip("qkv", got, ref):
+        assert wrongly_rounded(a, r) <= 2.0 ** -11, name
