@@ -383,15 +383,16 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
       for (int i = 0; i < 2; ++i) {
         const float2 eg = *reinterpret_cast<const float2*>(gate + 8 * i);
         const float2 v0 = unpack_bf16x2(v[2 * i]), v1 = unpack_bf16x2(v[2 * i + 1]);
-        X[i][0] = v0.x - eg.x * X[i][0];
-        X[i][1] = v0.y - eg.y * X[i][1];
-        X[i][2] = v1.x - eg.x * X[i][2];
-        X[i][3] = v1.y - eg.y * X[i][3];
+        // a decay of zero clears a state that is not finite too
+        X[i][0] = eg.x == 0.f ? v0.x : v0.x - eg.x * X[i][0];
+        X[i][1] = eg.y == 0.f ? v0.y : v0.y - eg.y * X[i][1];
+        X[i][2] = eg.x == 0.f ? v1.x : v1.x - eg.x * X[i][2];
+        X[i][3] = eg.y == 0.f ? v1.y : v1.y - eg.y * X[i][3];
         if constexpr (!SAVE) {
-          O[i][0] *= a.scale * eg.x;
-          O[i][1] *= a.scale * eg.y;
-          O[i][2] *= a.scale * eg.x;
-          O[i][3] *= a.scale * eg.y;
+          O[i][0] = eg.x == 0.f ? 0.f : a.scale * eg.x * O[i][0];
+          O[i][1] = eg.y == 0.f ? 0.f : a.scale * eg.y * O[i][1];
+          O[i][2] = eg.x == 0.f ? 0.f : a.scale * eg.x * O[i][2];
+          O[i][3] = eg.y == 0.f ? 0.f : a.scale * eg.y * O[i][3];
         }
       }
       put_tiles<3>(own + W::kX, w, X[0], X[1], lane);
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
       float acc[DK / 32][4];
       load_rows<DK>(bk, sk, w, lane);
       const float last = reinterpret_cast<const float*>(st + W::kGate)[63];
+      if (last == 0.f) zero(S);  // (what is not finite among it)
       team_bar(slice);
       // S <- e^{G_63} S + (e^{G_63 - G} U)^T K, this warp's columns
       outer_rows<DK>(acc, own + W::kW, bk, lane);
@@ -564,6 +566,9 @@ __global__ void __launch_bounds__(32 * kRecWarps) delta_recurrent_kernel(DeltaAr
   for (int t = 0; t < len; ++t) {
     const float4 kc = k, qc = q;
     const float vc = v, alpha = expf(gt), bc = bt;
+    if (alpha == 0.f)  // clears a state that is not finite too
+#pragma unroll
+      for (int j = 0; j < kRecRows; ++j) S[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t + 1 < len) fetch(t + 1);
     float x[16];
 #pragma unroll

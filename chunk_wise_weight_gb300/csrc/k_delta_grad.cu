@@ -293,7 +293,7 @@ __device__ __forceinline__ void gate_gradient(const KeySums& s, int set, float* 
   }
 #pragma unroll
   for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(~0u, d, m);
-  d *= s.gate[set][0][63];
+  d = s.gate[set][0][63] == 0.f ? 0.f : d * s.gate[set][0][63];
   float after = a[0] + a[1], before = c[0] + c[1];
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
           read16(trow + kTmS + quarter * HC + c0, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            v[e] *= m;
+            v[e] = eg == 0.f ? 0.f : v[e] * m;  // (a state before a reset may be anything)
             acc[c0 + e] += v[e];
           }
           part_a += dot_row(c0 / 8, v) + dot_row(c0 / 8 + 1, v + 8);

@@ -433,22 +433,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       const uint32_t par = c & 1;
       again(row, quarter);
       if (c > 0) finish_state(c - 1);
+      const unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
       put_s();
       arrive(&bars->s_ready);
       if constexpr (SAVE) snap_s(c);
       if (c > 0) finish_out(c - 1);
-      const unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
       const float4* gate = reinterpret_cast<const float4*>(rest + W::kGate) + quarter * (kTok / 4);
       const unsigned char* vcol = rest + W::kV + kTok * quarter * 256 + row * 2;
       float x[kTok];
       __nv_bfloat16 v[kTok];
       wait(&bars->full[st], (c >> 1) & 1);
+      const bool reset = *reinterpret_cast<const float*>(rest + W::kGate) == 0.f;  // clears what is not finite too
 #pragma unroll
       for (int e = 0; e < kTok; ++e) v[e] = *reinterpret_cast<const __nv_bfloat16*>(vcol + e * 256);
       wait(&bars->p_done, par);
       tc_fence_after_sync();
       // X = V - e^G (K S^T)
       read16(trow + kTmP + kTok * quarter, x);
+      if (reset) {
+#pragma unroll
+        for (int i = 0; i < HS; ++i) S[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kTok; ++e) x[e] = 0.f;
+      }
 #pragma unroll
       for (int e = 0; e < kTok; e += 4) {
         const float4 eg = gate[e / 4];
@@ -470,6 +477,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
           O[e + 2] *= a.scale * eg.z;
           O[e + 3] *= a.scale * eg.w;
         }
+        if (reset)
+#pragma unroll
+          for (int e = 0; e < kTok; ++e) O[e] = 0.f;
       }
       float ge[kTok];
 #pragma unroll

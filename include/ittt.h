@@ -494,13 +494,17 @@ ITTT_API size_t ittt_layer_norm_grad_workspace_bytes(int64_t N, int64_t d);
  *   v, out  [B,T,Hv,dv]; Hv a multiple of Hk (value head h reads key head
  *           h / (Hv / Hk)); dv a multiple of 16 up to 512.  q, k and v share
  *           one type; out may be bf16 or fp32.
- *   g       fp32 [B,T,Hv], log decays; -inf resets the state.
+ *   g       fp32 [B,T,Hv], log decays (not positive); -inf resets the state:
+ *           what follows depends on nothing finite before it.
  *   beta    fp32 [B,T,Hv].  g and beta may have any non-negative strides.
  *
  * bf16 sequences of more than 16 tokens run in chunks of 64 on the tensor
  * cores, the state carried with fp32 accuracy (24 bits); shorter ones, and
  * fp32 inputs at any length, run token by token in fp32.  A value that is
- * not finite can reach every output of its chunk and of later ones.
+ * not finite can reach every output of its chunk and of later ones; token by
+ * token every reset clears it, in chunks those at a chunk's first token (the
+ * first of a sequence, and every 64th from there), so a sequence that starts
+ * with a reset may start from a state_in that was never written.
  */
 typedef struct {
   const ittt_tensor* state_in; /* fp32 [S,Hv,dv,dk] or NULL (zero); S = B, or num_docs */
@@ -555,8 +559,8 @@ ITTT_API size_t ittt_delta_grad_workspace_bytes(int64_t B, int64_t T, int64_t Hv
  * [B,Hv,dv], g, beta [B,Hv] as above; state is a pool fp32 [S,Hv,dv,dk] that
  * is updated in place.  Sequence i uses row slots[i] (int32 or int64 [B];
  * NULL: row i, then S = B); a slot outside [0,S) marks a row of the batch
- * that holds no sequence: its output is zero and no state changes.  Slots
- * must be distinct.  Allocates nothing and can be captured into a graph.
+ * that holds no sequence: its output is zero and no state changes.  A reset
+ * clears any row, one that was never written too.  Slots must be distinct.  Allocates nothing and can be captured into a graph.
  */
 ITTT_API ittt_status ittt_delta_step(const ittt_tensor* q, const ittt_tensor* k,
                                      const ittt_tensor* v, const ittt_tensor* g,
