@@ -170,9 +170,13 @@ def _ref(desc):
 
 
 def _stream_handle(stream, device) -> int:
-    if stream is None:
-        if isinstance(device, torch.device) and device.index is not None:
+    if isinstance(device, torch.device) and device.type == "cuda" and device.index is not None:
+        # the library's launches follow the current device
+        if device.index != torch._C._cuda_getDevice():
+            raise ValueError(f"tensors on GPU {device.index}, but GPU {torch._C._cuda_getDevice()} is current")
+        if stream is None:
             return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream is None:
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -361,26 +365,37 @@ _pack_tensor = struct.Struct("Pii8q").pack  # the layout of ittt_tensor
 _PAD = tuple((0,) * (4 - n) for n in range(5))
 
 
-def _desc(t: torch.Tensor | None) -> bytes | None:
-    """An ittt_tensor as bytes (what describe() fills field by field: these
-    calls take a few microseconds on the GPU, and their host side counts)."""
-    if t is None:
-        return None
-    dtype = _ALL_DTYPES.get(t.dtype)
-    if dtype is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("expected CUDA tensors")
-    n = t.dim()
-    if n > 4:
-        raise ValueError("at most 4 dimensions")
-    pad = _PAD[n]
-    return _pack_tensor(t.data_ptr(), dtype, n, *t.shape, *pad, *t.stride(), *pad)
+def _descs(*tensors) -> list:
+    """ittt_tensors of one call as bytes (what describe() fills field by field:
+    these calls take a few microseconds on the GPU, and their host side counts).
+    All have to be on one GPU."""
+    out, gpu = [], None
+    for t in tensors:
+        if t is not None:
+            dtype = _ALL_DTYPES.get(t.dtype)
+            if dtype is None:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            at = t.get_device()
+            if at != gpu:
+                if at < 0:
+                    raise ValueError("expected CUDA tensors")
+                if gpu is not None:
+                    raise ValueError(f"tensors on GPU {gpu} and on GPU {at}")
+                gpu = at
+            n = t.dim()
+            if n > 4:
+                raise ValueError("at most 4 dimensions")
+            pad = _PAD[n]
+            t = _pack_tensor(t.data_ptr(), dtype, n, *t.shape, *pad, *t.stride(), *pad)
+        out.append(t)
+    return out
 
 
-def _workspace(workspace) -> tuple:
+def _workspace(workspace, like: torch.Tensor) -> tuple:
     if workspace is None:
         return None, 0
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the GPU of the others")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -398,8 +413,8 @@ def embed(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
     if out is None:
         out = torch.empty(*ids.shape, table.shape[-1], dtype=out_dtype or table.dtype,
                           device=table.device)
-    _check(lib.ittt_embed(_desc(ids), _desc(table), scale, _desc(out),
-                          _stream_handle(stream, table.device)))
+    ids, rows, to = _descs(ids, table, out)
+    _check(lib.ittt_embed(ids, rows, scale, to, _stream_handle(stream, table.device)))
     return out
 
 
@@ -416,8 +431,9 @@ def embed_grad(ids: torch.Tensor, grad_out: torch.Tensor, rows: int, scale: floa
         grad = torch.empty(rows, grad_out.shape[-1], dtype=grad_dtype, device=grad_out.device)
     elif grad.shape[0] != rows:
         raise ValueError(f"grad has {grad.shape[0]} rows, expected {rows}")
-    _check(lib.ittt_embed_grad(_desc(ids), _desc(grad_out), scale, int(accumulate), _desc(grad),
-                               *_workspace(workspace), _stream_handle(stream, grad_out.device)))
+    ids, dy, to = _descs(ids, grad_out, grad)
+    _check(lib.ittt_embed_grad(ids, dy, scale, int(accumulate), to, *_workspace(workspace, grad_out),
+                               _stream_handle(stream, grad_out.device)))
     return grad
 
 
@@ -440,8 +456,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         mean = mean.view(-1)
     if rstd is not None and rstd.dim() != 1:
         rstd = rstd.view(-1)
-    _check(lib.ittt_layer_norm(_desc(x), _desc(weight), _desc(bias), eps, _desc(out), _desc(mean),
-                               _desc(rstd), _stream_handle(stream, x.device)))
+    *ins, to, mean, rstd = _descs(x, weight, bias, out, mean, rstd)
+    _check(lib.ittt_layer_norm(*ins, eps, to, mean, rstd, _stream_handle(stream, x.device)))
     return out
 
 
@@ -460,9 +476,8 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     if grad_bias is None:
         grad_bias = torch.empty_like(weight)
     _check(lib.ittt_layer_norm_grad(
-        *[_desc(t) for t in (grad_out, x, weight, mean.view(-1), rstd.view(-1), grad_x,
-                             grad_weight, grad_bias)],
-        *_workspace(workspace), _stream_handle(stream, x.device)))
+        *_descs(grad_out, x, weight, mean.view(-1), rstd.view(-1), grad_x, grad_weight, grad_bias),
+        *_workspace(workspace, x), _stream_handle(stream, x.device)))
     return grad_x, grad_weight, grad_bias
 
 
@@ -471,11 +486,13 @@ def layer_norm_grad_workspace_bytes(n: int, d: int) -> int:
     return int(load().ittt_layer_norm_grad_workspace_bytes(n, d))
 
 
-def _delta_opts(opts, keep: dict, cu_seqlens, workspace, **tensors):
+def _delta_opts(opts, keep: dict, cu_seqlens, workspace, like: torch.Tensor, **tensors):
     for name, t in tensors.items():
         if t is not None:
             if not t.is_cuda:
                 raise ValueError("expected CUDA tensors")
+            if t.get_device() != like.get_device():
+                raise ValueError(f"{name}: on GPU {t.get_device()}, the others are on GPU {like.get_device()}")
             keep[name] = describe(t)
             setattr(opts, name, ctypes.pointer(keep[name]))
     arr = _seqlens(cu_seqlens)
@@ -483,7 +500,7 @@ def _delta_opts(opts, keep: dict, cu_seqlens, workspace, **tensors):
         keep["cu_seqlens"] = arr
         opts.cu_seqlens = ctypes.cast(arr, ctypes.POINTER(ctypes.c_int64))
         opts.num_docs = len(arr) - 1
-    opts.workspace, opts.workspace_bytes = _workspace(workspace)
+    opts.workspace, opts.workspace_bytes = _workspace(workspace, like)
     return opts
 
 
@@ -501,10 +518,10 @@ def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     if out is None:
         out = _like(v, out_dtype)
     extra = {}
-    opts = _delta_opts(DeltaOpts(), extra, cu_seqlens, workspace, state_in=state_in,
+    *ins, to = _descs(q, k, v, g, beta, out)
+    opts = _delta_opts(DeltaOpts(), extra, cu_seqlens, workspace, v, state_in=state_in,
                        state_out=state_out)
-    _check(lib.ittt_delta_rule(*[_desc(t) for t in (q, k, v, g, beta)],
-                               q.shape[-1] ** -0.5 if scale is None else scale, _desc(out),
+    _check(lib.ittt_delta_rule(*ins, q.shape[-1] ** -0.5 if scale is None else scale, to,
                                _stream_handle(stream, v.device), ctypes.byref(opts)))
     return out
 
@@ -528,11 +545,10 @@ def delta_rule_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     grads = [_like(t, torch.bfloat16) for t in (q, k, v)] + [_like(t, torch.float32)
                                                              for t in (g, beta)]
     extra = {}
-    opts = _delta_opts(DeltaGradOpts(), extra, cu_seqlens, workspace, state_in=state_in,
+    descs = _descs(q, k, v, g, beta, grad_out, *grads)
+    opts = _delta_opts(DeltaGradOpts(), extra, cu_seqlens, workspace, v, state_in=state_in,
                        grad_state_out=grad_state_out, grad_state_in=grad_state_in)
-    _check(lib.ittt_delta_rule_grad(*[_desc(t) for t in (q, k, v, g, beta, grad_out)],
-                                    q.shape[-1] ** -0.5 if scale is None else scale,
-                                    *[_desc(t) for t in grads],
+    _check(lib.ittt_delta_rule_grad(*descs[:6], q.shape[-1] ** -0.5 if scale is None else scale, *descs[6:],
                                     _stream_handle(stream, v.device), ctypes.byref(opts)))
     return tuple(grads)
 
@@ -554,7 +570,7 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     lib = load()
     if out is None:
         out = _like(v, out_dtype)
-    _check(lib.ittt_delta_step(*[_desc(t) for t in (q, k, v, g, beta, state, slots)],
-                               q.shape[-1] ** -0.5 if scale is None else scale, _desc(out),
+    *ins, to = _descs(q, k, v, g, beta, state, slots, out)
+    _check(lib.ittt_delta_step(*ins, q.shape[-1] ** -0.5 if scale is None else scale, to,
                                _stream_handle(stream, v.device)))
     return out
