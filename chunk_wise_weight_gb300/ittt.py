@@ -360,6 +360,8 @@ def version() -> int:
 
 
 # ---------------------------------------------- operators around the layer
+# No call here is recorded by automatic differentiation: results of tensors that
+# require gradients are detached, and the *_grad calls give the gradients.
 _ALL_DTYPES = _DTYPES | _INT_DTYPES
 _pack_tensor = struct.Struct("Pii8q").pack  # the layout of ittt_tensor
 _PAD = tuple((0,) * (4 - n) for n in range(5))

@@ -9,7 +9,9 @@ Two fast weights work side by side: the delta rule's, written once a token, and
 the layer's W_down, written once a chunk.  `prefill` runs whole prompts,
 `decode` one token of each running sequence on pools of both states, and
 `train` takes gradient steps on the mixer (lookup, norms, projections, delta
-rule) with automatic differentiation around the operators' gradients.
+rule) with automatic differentiation around the operators' gradients: the calls
+themselves are not recorded, Embed, LayerNorm and DeltaRule below record them, once
+(a second derivative is an error).
 
     python examples/fast_weight_model.py
 """
@@ -19,6 +21,7 @@ import time
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from chunk_wise_weight_gb300 import build, ittt  # noqa: E402
@@ -32,6 +35,7 @@ class Embed(torch.autograd.Function):
         return ittt.embed(ids, table, scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
         return None, ittt.embed_grad(ids, dy.contiguous(), ctx.rows, ctx.scale, grad_dtype=ctx.dtype), None
@@ -46,6 +50,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return ittt.layer_norm_grad(dy.contiguous(), *ctx.saved_tensors)
 
@@ -57,6 +62,7 @@ class DeltaRule(torch.autograd.Function):
         return ittt.delta_rule(q, k, v, g, beta)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return ittt.delta_rule_grad(*ctx.saved_tensors, dy.contiguous())
 
