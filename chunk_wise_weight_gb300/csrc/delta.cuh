@@ -478,9 +478,12 @@ __device__ __forceinline__ void init_bars(StageBars* bars) {
   }
   __syncthreads();
 }
-__device__ __forceinline__ void wait_block(StageBars* bars, int it, unsigned int* status) {
-  if (!mbar_wait(&bars->full[it & 1], (it >> 1) & 1, &bars->abort))
-    raise_abort(&bars->abort, status, kStatusTimeout);
+// Whether the wait has run out: the CTA then stops at the chunk's next barrier, all
+// roles together, before another copy is issued.
+__device__ __forceinline__ bool wait_block(StageBars* bars, int it, unsigned int* status) {
+  const bool late = !mbar_wait(&bars->full[it & 1], (it >> 1) & 1, &bars->abort);
+  if (late) raise_abort(&bars->abort, status, kStatusTimeout);
+  return late;
 }
 
 // A [64 x dim] tile by one warp: 16-byte pieces, rows of the tile `st` elements

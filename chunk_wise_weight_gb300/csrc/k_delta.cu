@@ -354,8 +354,10 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
         load_cols(st + W::kCols, vp + t * a.v.st, a.v.st, pieces, n, a.v.vec, lane, 32);
         cp_wait_all();
       }
-      __syncthreads();  // chunk c is in its stage; the teams are done with chunk c - 1
+      // chunk c is in its stage; the teams are done with chunk c - 1
+      if (__syncthreads_or(0)) break;
     }
+    settle(&bars->abort);
     return;
   }
 
@@ -366,9 +368,10 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
     return SAVE && c < nchunks ? a.save.snap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK) : nullptr;
   };
   put_state<DK, SAVE>(own, S, w, lane, snapshot(0), row0, a.dv);
-  for (int c = 0; c < nchunks; ++c) {
-    __syncthreads();
-    wait_block(bars, c, a.status);
+  bool late = false;
+  for (int c = 0;; ++c) {
+    if (__syncthreads_or(late) || c == nchunks) break;
+    late = wait_block(bars, c, a.status);
     const unsigned char* st = smem + (c & 1) * stage_bytes;
     const uint32_t sk = smem_u32(st), se = sk + W::kMap;
     const float* gate = reinterpret_cast<const float*>(st + W::kGate) + 16 * w + t2;  // this warp's tokens
@@ -463,7 +466,6 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_walk_kernel(WalkArgs a) 
                    int64_t(a.Hv) * a.dv, n, lane);
     }
   }
-  __syncthreads();
   if (a.state_out) store_state<DK>(S, a.state_out, srow, w, lane);
 }
 

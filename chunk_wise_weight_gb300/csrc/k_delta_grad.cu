@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
         load_cols(st + W::kCols, dop + t * a.dout.st, a.dout.st, pieces, n, a.dout.vec, lane, 32);
         cp_wait_all();
       }
-      __syncthreads();
+      if (__syncthreads_or(0)) break;
     }
+    settle(&bars->abort);
     return;
   }
 
@@ -108,10 +109,11 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
     return c < 0 ? nullptr : a.dsnap + ((chunk0 + c) * a.Hv + h) * state_parts(a.dv, DK);
   };
   put_state<DK, true>(own, S, w, lane, snapshot(nchunks - 1), row0, a.dv);
-  for (int it = 0; it < nchunks; ++it) {
+  bool late = false;
+  for (int it = 0;; ++it) {
+    if (__syncthreads_or(late) || it == nchunks) break;
     const int c = nchunks - 1 - it;
-    __syncthreads();
-    wait_block(bars, it, a.status);
+    late = wait_block(bars, it, a.status);
     const unsigned char* st = smem + (it & 1) * stage_bytes;
     const uint32_t sk = smem_u32(st), sq = sk + W::kTile;
     const uint32_t sd = sk + W::kCols + 32 * slice;
@@ -212,7 +214,6 @@ __global__ void __launch_bounds__(2 * kTeam + 32) delta_reverse_kernel(ReverseAr
     store_tokens(R, own + W::kX + w * 3 * kOperand, a.dvp + (orow * a.Hv + h) * a.dv + row0, int64_t(a.Hv) * a.dv,
                  n, lane);
   }
-  __syncthreads();
   if (a.dstate_in) store_state<DK>(S, a.dstate_in, srow, w, lane);
 }
 
@@ -369,12 +370,14 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   // Loads of a panel's operands, by one thread: three parts each.
   auto head = [&](int h) { return int64_t(chunk) * a.Hv + h; };
   auto load_states = [&](const unsigned char* from, int h, int v0, uint32_t to, uint64_t* bar) {
+    if (aborted(&bars->abort)) return;
     const uint32_t bytes = uint32_t(min(kPanel, a.dv - v0)) * DK * 2;
     from += head(h) * state_parts(a.dv, DK) + state_parts(v0, DK);
     mbar_arrive_expect_tx(bar, 3 * bytes);
     for (int p = 0; p < 3; ++p) bulk_load(smem + to + p * W::kStatePart, from + p * bytes, bytes, bar);
   };
   auto load_tokens = [&](const unsigned char* from, int h, int v0, uint32_t to, uint64_t* bar) {
+    if (aborted(&bars->abort)) return;
     const uint32_t bytes = uint32_t(min(kPanel, a.dv - v0)) * 128;
     from += head(h) * token_tiles(a.dv) + int64_t(v0) * 128;
     mbar_arrive_expect_tx(bar, 3 * bytes);
@@ -713,6 +716,7 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
       *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+  settle(&bars->abort);
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 0) {

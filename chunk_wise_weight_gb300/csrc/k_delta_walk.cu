@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
       for (int c = 0; c < nchunks; ++c, tile += kDeltaChunk * tile_st, plain += kDeltaChunk * plain_st) {
         const int st = c & 1, n = min(kDeltaChunk, len - c * kDeltaChunk);
         if (c >= 2) wait(&bars->empty[st], ((c >> 1) & 1) ^ 1);
+        if (__any_sync(~0u, aborted(&bars->abort))) break;
         unsigned char* tiles = smem + st * W::kTiles;
         unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
         if (lw == 0 && lane == 0) {
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_walk_kernel(TcArgs a) {
         *reinterpret_cast<float4*>(a.state_out + srow + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     tc_fence_before_sync();
   }
+  settle(&bars->abort);
   __syncthreads();
   tc_fence_after_sync();
   if (warp == kTcWarps) tmem_dealloc(tm, 512);
@@ -642,6 +644,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
         unsigned char* tiles = smem + st * W::kTiles;
         unsigned char* rest = smem + 2 * W::kTiles + st * W::kRest;
         if (it >= 2) wait(&bars->empty[st], ((it >> 1) & 1) ^ 1);
+        if (__any_sync(~0u, aborted(&bars->abort))) break;
         if (lw == 0 && lane == 0) {
           const unsigned char* blk = a.blocks + ((chunk0 + c) * a.Hv + h) * int64_t(kWideGrad);
           mbar_arrive_expect_tx(&bars->full[st], 6 * kWideTile + 768);
@@ -849,6 +852,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) head_reverse_kernel(ReverseArgs
         *reinterpret_cast<float4*>(a.dstate_in + srow + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     tc_fence_before_sync();
   }
+  settle(&bars->abort);
   __syncthreads();
   tc_fence_after_sync();
   if (warp == kTcWarps) tmem_dealloc(tm, 512);

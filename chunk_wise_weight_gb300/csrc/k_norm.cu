@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(THREADS, CTAS)
   }
   for (int64_t r0 = int64_t(blockIdx.x) * R; r0 < a.N; r0 += step, par ^= 1, ++it) {
     const int stage = it % stages;
-    if (VEC && !mbar_wait(&bars.full[stage], (it / stages) & 1, &bars.abort))
+    bool loaded = true;
+    if (VEC && !(loaded = mbar_wait(&bars.full[stage], (it / stages) & 1, &bars.abort)))
       raise_abort(&bars.abort, status, kStatusTimeout);
     P px[R][NV], pg[R][NV];
     float mean[R], rstd[R];
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
     }
     block_sums<2 * R>(s, buf[par]);
     // every thread is past the barrier: the stage is read
-    if (VEC && threadIdx.x == 0) fetch(stage, r0 + stages * step);
+    if (VEC && threadIdx.x == 0 && loaded) fetch(stage, r0 + stages * step);
     if (dx == nullptr) continue;
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(THREADS, CTAS)
           }
       }
   }
+  if (VEC) settle(&bars.abort);
   // This CTA's share of dw and db: [2][gridDim.x][d].
   if (a.dw == nullptr && a.db == nullptr) return;
 #pragma unroll

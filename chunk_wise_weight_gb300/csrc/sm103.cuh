@@ -113,6 +113,19 @@ __device__ __forceinline__ void raise_abort(volatile int* abort_flag, unsigned i
   atomicOr(status, bits);
 }
 
+// For kernels whose roles run on through their loops after a wait has run out (every
+// later wait fails at once): from then on no copy is issued, since its barrier may be a
+// phase behind, and before the CTA ends, what was issued gets a millisecond, a thousand
+// times what a copy or a product takes, to land.
+__device__ __forceinline__ bool aborted(const int* abort_flag) {
+  return *static_cast<const volatile int*>(abort_flag) != 0;
+}
+__device__ __forceinline__ void settle(const int* abort_flag) {
+  if (aborted(abort_flag))
+    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
+    }
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
