@@ -449,8 +449,9 @@ ITTT_API ittt_status ittt_embed(const ittt_tensor* ids, const ittt_tensor* table
  * The lookup's gradient: grad_table[r] = scale * sum over n with ids[n] = r
  * of grad_out[n], every other row zero; or, with `accumulate`, added to an
  * fp32 grad_table (rows that do not occur are not touched).  Sums are formed
- * in fp32 in the order of the positions, with no atomics on floats: equal
- * calls give equal bits.  ids outside [0,V) are dropped.
+ * in fp32, with no atomics on floats, in an order that the ids fix (partial sums
+ * over neighbouring positions, then their sum; not one addition after another by
+ * position): equal calls give equal bits.  ids outside [0,V) are dropped.
  */
 ITTT_API ittt_status ittt_embed_grad(const ittt_tensor* ids, const ittt_tensor* grad_out,
                                      float scale, int32_t accumulate, ittt_tensor* grad_table,
