@@ -21,8 +21,8 @@
 //
 // Four kernels: the chunks' blocks and the forward walk (k_delta.cu) keep S and E; a
 // reverse walk, of the same shape, carries dS and leaves dR and dS'; then everything
-// else, of every chunk at once.  2 x 4096 tokens, 20 heads of 128 x 128: 95 + 276 + 338 +
-// 345 us; bound by the two walks' chains and by the last kernel's passes, whose products
+// else, of every chunk at once.  2 x 4096 tokens, 20 heads of 128 x 128: 95 + 277 + 338 +
+// 311 us; bound by the two walks' chains and by the last kernel's passes, whose products
 // and sums take turns.
 #include <algorithm>
 
@@ -226,17 +226,11 @@ struct KeyGradArgs {
   float scale;
   const unsigned char* blocks;
   const unsigned char *snap, *dsnap, *e, *dr;
-  int ahead;                     // CTAs between one and the next on its SM
   int64_t block_bytes, gate_at;  // a chunk's block, and the gates in it
   __nv_bfloat16 *dq, *dk;
   float *dg, *dbeta;
   unsigned int* status;
 };
-
-__device__ __forceinline__ void prefetch_bulk(const unsigned char* from, int64_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(from)), "r"(uint32_t(bytes))
-               : "memory");
-}
 
 constexpr int kKeyThreads = 512;
 
@@ -326,8 +320,10 @@ __device__ __forceinline__ void gate_gradient(const KeySums& s, int set, float* 
 // zero (in tensor memory dbeta's error in the Frobenius norm was 7.7e-7, now 3.1e-7).
 // What a pass has used up is loaded anew at once, so that the next one's operands
 // arrive under its remaining products and sums.  128 chunks of 10 key heads, two value
-// heads of 128 x 128 each: 345 us, of which 112 would be the bytes (755 MB, mostly
+// heads of 128 x 128 each: 311 us, of which 112 would be the bytes (755 MB, mostly
 // states) and 130 the products; products and the sums that wait for them take turns.
+// (With the next head's operands prefetched into L2 as well some 40 us more: they are
+// evicted again, and a quarter of the bytes is read twice.)
 template <int DK>
 __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradArgs a) {
   extern __shared__ unsigned char smem_raw[];
@@ -440,16 +436,6 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
   const uint32_t tmu = __shfl_sync(~0u, tm, 0);
   auto lo = [&](uint32_t at, uint32_t lbo = 16) { return base + ((at >> 4) | (lbo >> 4) << 16); };
   auto below = [&](uint32_t at) { return base + ((W::kZero >> 4) | ((at - W::kZero) >> 4) << 16); };
-  // A head's operands, most of what is read, come as far as L2 while the products
-  // of the one before run, this CTA's or the last one's on this SM.
-  auto fetch = [&](int64_t linear, int h_next) {
-    const int64_t at = (linear % gridDim.x) * a.Hv + h_next;
-    prefetch_bulk(a.snap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
-    prefetch_bulk(a.dr + at * token_tiles(a.dv), token_tiles(a.dv));
-    prefetch_bulk(a.e + at * token_tiles(a.dv), token_tiles(a.dv));
-    prefetch_bulk(a.dsnap + at * state_parts(a.dv, DK), state_parts(a.dv, DK));
-  };
-  const int64_t here = int64_t(blockIdx.y) * gridDim.x + blockIdx.x, after = here + a.ahead;
   float acc[HC], P[16];
 #pragma unroll
   for (int e = 0; e < HC; ++e) acc[e] = 0.f;
@@ -497,13 +483,6 @@ __global__ void __launch_bounds__(kKeyThreads, 1) delta_key_grad_kernel(KeyGradA
         wait(&bars->r, par);
         wait(&bars->e, par);
         wait(&bars->s, par);
-        if (v0 == 0 && lane == 0) {
-          if (h + 1 < h_end)
-            fetch(here, h + 1);
-          else if (after < int64_t(gridDim.x) * gridDim.y)
-            fetch(after, int(after / gridDim.x) * group);
-        }
-        __syncwarp();
         // small terms first; dO is exact, so it has no other parts (unrolled: with
         // descriptors worked out in loops, each product cost its issuer 100 cycles)
 #pragma unroll
@@ -815,7 +794,6 @@ cudaError_t launch_delta_grad(const LaunchEnv& env, const DeltaGradArgs& a) {
   g.dsnap = r.dsnap;
   g.e = save.e;
   g.dr = r.dr;
-  g.ahead = env.num_sms;
   g.status = env.status;
   g.dq = static_cast<__nv_bfloat16*>(a.dq);
   g.dk = static_cast<__nv_bfloat16*>(a.dk);
