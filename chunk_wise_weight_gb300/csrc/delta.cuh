@@ -593,7 +593,7 @@ __device__ __forceinline__ void store_row_sums(float (&x)[16], float* to, int la
 // Slices a CTA of a walk: one while every slice has an SM of its own, two beyond
 // that, which share the loads of K, Q and the chunk's block and fill each other's
 // waits.  1024 tokens, heads of 128 x 128, one / two slices a CTA: 16 heads (128
-// slices) 53 / 70 us, gradient 185 / 226; 20 heads (160) 88 / 70 us, 308 / 244.
+// slices) 55 / 74 us, gradient 160 / 188; 20 heads (160) 98 / 74 us, 234 / 210.
 inline int walk_slices(int ndocs, int Hv, int dv, int num_sms) {
   return dv % 32 == 0 && int64_t(ndocs) * Hv * (dv / 16) > num_sms ? 2 : 1;
 }

@@ -11,9 +11,9 @@
 // The inverse and M depend on q, k, g and b alone: a first kernel forms them
 // for all chunks at once.  The second walks the chunks in order.
 //
-// 8192 tokens, 20 heads of 128 x 128 (10 key heads): 48 + 434 us.  The call's bytes
+// 8192 tokens, 20 heads of 128 x 128 (10 key heads): 48 + 443 us.  The call's bytes
 // would pass in 19 us and its products in 10; it is bound by the chain of 128
-// chunks, 3.4 us each, of three products that wait for one another (token by token
+// chunks, 3.5 us each, of three products that wait for one another (token by token
 // it would be 8192 steps of 0.9 us).  The output's products have 24-bit operands too,
 // so that a bf16 output is the exact one's rounding; with 16 bits, which moved 0.3% of
 // the outputs to the other neighbour, the walk took 398 us (heads of 64 x 64: 4096
@@ -647,11 +647,11 @@ cudaError_t launch_delta_prepare(const LaunchEnv& env, const DeltaArgs& a, unsig
 // A team walks a slice of 16 rows, two to four slices an SM; a whole head an SM
 // wins from the next round of slices on, unless it fills less than half of the
 // tensor cores' 128 rows.  1024 tokens, heads of 128 x dv, us by slice / by head:
-//   dv 128: 36 heads (288 slices) 72 / 80, 40 heads (320) 129 / 88
-//   dv 64: 72 heads (288) 86 / 90, 80 heads (320) 143 / 96
-//   dv 256: 16 heads (256) 68 / 76, 20 heads (320) 121 / 78
-//   dv 32: 128 heads (256) 104 / 111, 160 heads (320) 166 / 174, 320 heads 268 / 283
-// and the gradient alike (dv 128: 257 / 283, then 442 / 302; dv 32: 1083 / 1009).
+//   dv 128: 36 heads (288 slices) 78 / 84, 40 heads (320) 139 / 90
+//   dv 64: 72 heads (288) 90 / 92, 80 heads (320) 152 / 100
+//   dv 256: 16 heads (256) 74 / 78, 20 heads (320) 131 / 80
+//   dv 32: 128 heads (256) 109 / 115, 160 heads (320) 174 / 180, 320 heads 281 / 289
+// and the gradient alike (dv 128: 240 / 283, then 386 / 304; dv 32: 976 / 969).
 bool delta_by_head(int64_t sequences, int Hv, int dv, int num_sms) {
   return dv > 32 && sequences * Hv * (dv / 16) > 2 * num_sms;
 }

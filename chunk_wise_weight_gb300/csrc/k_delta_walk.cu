@@ -8,11 +8,11 @@
 // bounds it is their sum: 24 to 48 products of 64 columns (800 to 1600 cycles) and
 // then 1000 to 2000 cycles in which the 16 warps read, scale, split and write, at
 // 0.4 to 0.5 instructions a cycle and scheduler.  24001 tokens in 7 documents, 16
-// heads of 64 x 128: 277 us, as long as its longest document, 8600 cycles a chunk;
+// heads of 64 x 128: 277 us, as long as its longest document of 6712, 5000 cycles a chunk;
 // the gradient's walks of 2 x 4096 tokens, 20 heads of 128 x 128: 276 and 338 us,
-// 8400 and 10200 cycles a chunk (with the snapshots stored ahead of the products some
-// 40 us more; with shared memory read through generic addresses, whose registers then
-// spill, 20 to 40 more).
+// 8400 and 10200 cycles a chunk (measured on walks of 330 and 422 us, with snapshots
+// in other parts: snapshots stored ahead of the products 45 and 30 us more; shared
+// memory read through generic addresses, whose registers then spill, 43 and 20 more).
 #include <algorithm>
 
 #include "delta.cuh"

@@ -296,9 +296,9 @@ size_t table_bytes(int64_t num_docs) {
 
 // Sequences up to this long run token by token: a token's step costs about a
 // microsecond, a chunk of 64 some 20 us with its two launches.  Token by token /
-// by chunk, us: 20 heads of 128 x 128: 8 tokens 12 / 20, 16 tokens 20 / 20,
-// 24 tokens 27 / 20, 64 tokens 61 / 20; 64 sequences of 8 such heads: 8 tokens
-// 39 / 70, 16 tokens 64 / 72, 20 tokens 76 / 72, 64 tokens 219 / 76.
+// by chunk, us: 20 heads of 128 x 128: 8 tokens 12 / 18, 16 tokens 20 / 18,
+// 24 tokens 27 / 18, 64 tokens 61 / 18; 64 sequences of 8 such heads: 8 tokens
+// 39 / 66, 16 tokens 64 / 66, 20 tokens 78 / 68, 64 tokens 223 / 72.
 constexpr int64_t kRecurrentTokens = 16;
 bool chunked(const ittt::DeltaArgs& a, const DeltaDocs& d) {
   return !a.fp32 && d.longest > kRecurrentTokens;
