@@ -495,7 +495,7 @@ ITTT_API size_t ittt_layer_norm_grad_workspace_bytes(int64_t N, int64_t d);
  *   v, out  [B,T,Hv,dv]; Hv a multiple of Hk (value head h reads key head
  *           h / (Hv / Hk)); dv a multiple of 16 up to 512.  q, k and v share
  *           one type; out may be bf16 or fp32.
- *   g       fp32 [B,T,Hv], log decays (not positive); -inf resets the state:
+ *   g       fp32 [B,T,Hv], log decays; -inf resets the state:
  *           what follows depends on nothing finite before it.
  *   beta    fp32 [B,T,Hv].  g and beta may have any non-negative strides.
  *
